@@ -16,6 +16,7 @@ chunked round-robin copy plan of the prefetch (§4.3.2).
 Modules
   codecs    bf16 and OCP FP8 E4M3 rounding, written from the format definitions
   moe       routing, permutation, expert FFN, combine, fp8 block / group quantisation
+  layer     a model's gate and the RMS norms around the block
   prefetch  round-robin chunk plan of the layer-ahead expert prefetch
 
 Every function is pinned by the oracle self-tests (closed forms, brute force,

@@ -1,4 +1,4 @@
-"""ctypes loader for libdwdp.so, the C ABI declared in include/dwdp.h.
+"""ctypes loader for libdwdp.so, the C ABI declared in include/dwdp.h and include/dwdp_layer.h.
 
 The library is the only compute path: if it is not built, importing this
 module raises instead of falling back to anything else.
@@ -16,6 +16,7 @@ DWDP_OK, DWDP_ERR_INVALID_ARG, DWDP_ERR_UNSUPPORTED, DWDP_ERR_WORKSPACE, DWDP_ER
 F32, BF16, FP8_E4M3 = 0, 1, 2
 OP_PERMUTE, OP_GROUPED_FFN = 0, 1
 COPY_HIPMEMCPY, COPY_KERNEL, COPY_SDMA = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 
 
 class ExpertPtrs(ctypes.Structure):
@@ -36,6 +37,12 @@ class TileRecord(ctypes.Structure):
                 ("group", ctypes.c_int32), ("first_row", ctypes.c_int32), ("rows", ctypes.c_int32),
                 ("n_tile", ctypes.c_int32), ("group_m_tiles", ctypes.c_int32), ("xcd", ctypes.c_int32),
                 ("hw_id", ctypes.c_int32)]
+
+
+class GateArgs(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class DwdpError(RuntimeError):
@@ -77,6 +84,17 @@ SIGNATURES = {
     "dwdp_version": (ctypes.c_char_p, []),
 }
 
+# include/dwdp_layer.h
+_f32 = ctypes.c_float
+LAYER_SIGNATURES = {
+    "dwdp_route_gate": (_i32, [_vp, _vp, _i32, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dwdp_route_gate_workspace_bytes": (_sz, [_i64, _i32, _i32, _i32]),
+    "dwdp_gate_topk": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "dwdp_add_rmsnorm": (_i32, [_vp, _vp, _i32, _vp, _i32, _f32, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "dwdp_combine_add_rmsnorm": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _f32, _vp, _vp,
+                                        _vp, _vp, _vp]),
+}
+
 _lib = None
 
 
@@ -91,7 +109,7 @@ def load(path: str = LIB_PATH):
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is not built (run __graft_entry__.build()); there is no fallback path")
         lib = ctypes.CDLL(path)
-        for name, (res, args) in SIGNATURES.items():
+        for name, (res, args) in {**SIGNATURES, **LAYER_SIGNATURES}.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args

@@ -1,11 +1,13 @@
 """Thin Python binding of the C ABI (same names, argument marshalling only).
 
 torch tensors supply device memory and streams; every step of the MoE block
-runs in libdwdp.so's HIP kernels.  Shapes and dtypes follow include/dwdp.h.
+runs in libdwdp.so's HIP kernels.  Shapes and dtypes follow include/dwdp.h and,
+for the gate and the norms, include/dwdp_layer.h.
 """
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 
 import torch
 
@@ -183,6 +185,135 @@ def pack_weights(w, out, dtype_code_, stream=None):
     """Re-lay a weight matrix w [N, K] (bf16, or uint8 E4M3 codes) into the fragment-major layout in out."""
     N, K = w.shape
     _lib.check(_lib.load().dwdp_pack_weights(_ptr(w), N, K, dtype_code_, _ptr(out), _stream(stream)))
+
+
+# ------------------------------------------------------------------ around the block (include/dwdp_layer.h)
+#
+# These calls check their tensors before any address is passed on: the library sees addresses only, and a
+# wrong shape, type, layout or device would be read or written out of bounds there.
+
+_SCORES = {"softmax": _lib.SCORE_SOFTMAX, "sigmoid": _lib.SCORE_SIGMOID}
+
+
+@dataclass(frozen=True)
+class Gate:
+    """A model's gate (dwdp_gate): k experts by softmax or sigmoid score, out of the topk_groups best of
+    n_groups groups, with weights renormalised over the chosen and scaled."""
+    k: int
+    score: str = "softmax"
+    n_groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}, not {self.score!r}")
+        c = _lib.GateArgs(_SCORES[self.score], self.k, self.n_groups, self.topk_groups, self.group_top,
+                          int(self.renormalize), self.scale)
+        object.__setattr__(self, "_c", c)
+
+
+def _check(name, t, shape, dtypes, device):
+    """t's address, or None for None; ValueError unless t is a dense tensor of that shape, type and device."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be of type {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be dense and row-major (contiguous)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _check_device(name, t):
+    """t's device, which must be the current GPU: streams and launches belong to it."""
+    d = t.device
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {d}, which is not the current GPU")
+    return d
+
+
+def _matrix(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, not {t.dim()}")
+    return t.shape
+
+
+_ACT = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_U8 = (torch.uint8,)
+
+
+def route_gate_workspace_bytes(T: int, H: int, E: int, dtype: int) -> int:
+    return int(_lib.load().dwdp_route_gate_workspace_bytes(T, H, E, dtype))
+
+
+def route_gate(x, w_router, gate, logits_out, topk_idx, topk_w, ws=None, bias=None, balance_bias=None, stream=None):
+    """Router product and gate: x [T, H], w_router [E, H] -> logits_out [T, E], topk_idx, topk_w [T, k]."""
+    (T, H), E = _matrix("x", x), _matrix("w_router", w_router)[0]
+    dev = _check_device("x", x)
+    px = _check("x", x, (T, H), _ACT, dev)
+    pw = _check("w_router", w_router, (E, H), (x.dtype,), dev)
+    pl = _check("logits_out", logits_out, (T, E), _F32, dev)
+    pi = _check("topk_idx", topk_idx, (T, gate.k), _I32, dev)
+    pt = _check("topk_w", topk_w, (T, gate.k), _F32, dev)
+    pb = _check("bias", bias, (E,), _F32, dev)
+    pbb = _check("balance_bias", balance_bias, (E,), _F32, dev)
+    pws, nws = None, 0
+    if ws is not None:
+        nws = ws.numel() * ws.element_size()
+        pws = _check("ws", ws, ws.shape, (ws.dtype,), dev)
+    _lib.check(_lib.load().dwdp_route_gate(px, pw, dtype_code(x), pb, pbb, T, H, E, ctypes.byref(gate._c), pl, pi, pt,
+                                           pws, nws, _stream(stream)))
+
+
+def gate_topk(logits, gate, topk_idx, topk_w, balance_bias=None, stream=None):
+    """The gate alone: logits [T, E] -> topk_idx, topk_w [T, k]."""
+    T, E = _matrix("logits", logits)
+    dev = _check_device("logits", logits)
+    pl = _check("logits", logits, (T, E), _F32, dev)
+    pi = _check("topk_idx", topk_idx, (T, gate.k), _I32, dev)
+    pt = _check("topk_w", topk_w, (T, gate.k), _F32, dev)
+    pbb = _check("balance_bias", balance_bias, (E,), _F32, dev)
+    _lib.check(_lib.load().dwdp_gate_topk(pl, pbb, T, E, ctypes.byref(gate._c), pi, pt, _stream(stream)))
+
+
+def _norm_outputs(T, H, act, dev, residual, weight, sum_out, y, q, q_scale):
+    act = (act,)
+    return (_check("residual", residual, (T, H), act, dev), _check("weight", weight, (H,), _ACT, dev),
+            F32 if weight is None else dtype_code(weight), _check("sum_out", sum_out, (T, H), act, dev),
+            _check("y", y, (T, H), act, dev), _check("q", q, (T, H), _U8, dev),
+            _check("q_scale", q_scale, (T, H // 128), _F32, dev))
+
+
+def add_rmsnorm(x, residual, weight, eps, sum_out=None, y=None, q=None, q_scale=None, stream=None):
+    """z = x + residual; sum_out = z, y = z / rms(z) * weight, (q, q_scale) = y's E4M3 codes and 1x128 scales."""
+    T, H = _matrix("x", x)
+    dev = _check_device("x", x)
+    px = _check("x", x, (T, H), _ACT, dev)
+    pr, pw, wd, ps, py, pq, pqs = _norm_outputs(T, H, x.dtype, dev, residual, weight, sum_out, y, q, q_scale)
+    _lib.check(_lib.load().dwdp_add_rmsnorm(px, pr, dtype_code(x), pw, wd, eps, T, H, ps, py, pq, pqs,
+                                            _stream(stream)))
+
+
+def combine_add_rmsnorm(y_perm, inv_perm, topk_w, shared, residual, weight, eps, sum_out=None, y=None, q=None,
+                        q_scale=None, stream=None):
+    """The layer boundary: z = combine(y_perm) + residual; outputs as in add_rmsnorm (weight None: sum_out alone)."""
+    T, k = _matrix("inv_perm", inv_perm)
+    H = _matrix("y_perm", y_perm)[1]
+    dev = _check_device("y_perm", y_perm)
+    px = _check("y_perm", y_perm, (T * (k + shared), H), _ACT, dev)
+    pi = _check("inv_perm", inv_perm, (T, k), _I32, dev)
+    pt = _check("topk_w", topk_w, (T, k), _F32, dev)
+    pr, pw, wd, ps, py, pq, pqs = _norm_outputs(T, H, y_perm.dtype, dev, residual, weight, sum_out, y, q, q_scale)
+    _lib.check(_lib.load().dwdp_combine_add_rmsnorm(px, pi, pt, T, k, shared, H, dtype_code(y_perm), pr, pw, wd, eps, ps,
+                                                    py, pq, pqs, _stream(stream)))
 
 
 # ------------------------------------------------------------------ diagnostics (not steps of the block)

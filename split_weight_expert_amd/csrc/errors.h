@@ -30,6 +30,7 @@ inline int fail(int code, const std::string& msg) {
         if (!(cond)) return ::dwdp::fail(DWDP_ERR_INVALID_ARG, std::string(__func__) + ": " + (msg)); \
     } while (0)
 
+inline bool type_aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kFp8Group = 128;     // activation group width and weight block edge

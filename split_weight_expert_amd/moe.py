@@ -8,6 +8,10 @@ workspaces for a token count and runs route -> permute -> grouped FFN ->
 combine on one stream.  By default GEMM1 reads the token rows through the
 permutation (dwdp_moe_grouped_ffn_tokens) and no x_perm is materialised;
 gather=True runs the permute's row gather and the x_perm path instead.
+A model's own gate (api.Gate) takes the place of the plain softmax top-k, and
+norm / forward_normed run the block inside a pre-norm residual layer: the
+norm writes the block's input, and the block ends in the residual addition
+and the next layer's norm.
 Nothing here computes: every step is a libdwdp call.
 """
 from __future__ import annotations
@@ -127,13 +131,20 @@ class BlockBuffers:
     ws_perm: torch.Tensor
     ws_ffn: torch.Tensor
     x_tokens: torch.Tensor | None = None  # token mode: the rows GEMM1 reads (x, or x_q for fp8)
+    ws_route: torch.Tensor | None = None  # workspace of the gate's router product (None: it needs none)
+    x_norm: torch.Tensor | None = None    # normed layers: the block's input, written by the norm before it
 
 
 class MoEBlock:
-    """Route -> permute -> grouped SwiGLU FFN -> combine for one layer shape."""
+    """Route -> permute -> grouped SwiGLU FFN -> combine for one layer shape.
 
-    def __init__(self, H: int, I: int, E: int, k: int, shared: int, dtype: str, device="cuda", gather: bool = False):
-        self.H, self.I, self.E, self.k, self.shared = H, I, E, k, shared
+    gate: the model's gate (None: the softmax top-k of dwdp_route_topk)."""
+
+    def __init__(self, H: int, I: int, E: int, k: int, shared: int, dtype: str, device="cuda", gather: bool = False,
+                 gate: api.Gate | None = None):
+        if gate is not None and gate.k != k:
+            raise ValueError(f"the gate chooses {gate.k} experts, the block is for {k}")
+        self.H, self.I, self.E, self.k, self.shared, self.gate = H, I, E, k, shared, gate
         self.w_dtype = DTYPES[dtype]
         self.device = device
         self.gather = gather
@@ -150,6 +161,7 @@ class MoEBlock:
         g = self.gather
         ws_p = api.workspace_bytes(api.OP_PERMUTE, T, k, E, H, I, self.w_dtype, S)
         ws_f = api.workspace_bytes(api.OP_GROUPED_FFN, T, k, E, H, I, self.w_dtype, S)
+        ws_r = 0 if self.gate is None else api.route_gate_workspace_bytes(T, H, E, F32 if adt == torch.float32 else BF16)
         b = BlockBuffers(
             logits=torch.empty(T, E, dtype=torch.float32, device=dev),
             idx=torch.empty(T, k, dtype=torch.int32, device=dev),
@@ -165,11 +177,18 @@ class MoEBlock:
             y=torch.empty(T, H, dtype=adt, device=dev),
             ws_perm=torch.empty(max(ws_p, 256), dtype=torch.uint8, device=dev),
             ws_ffn=torch.empty(max(ws_f, 256), dtype=torch.uint8, device=dev),
+            ws_route=torch.empty(ws_r, dtype=torch.uint8, device=dev) if ws_r else None,
         )
         self._bufs[T] = b
         return b
 
-    def route(self, x, w_router, bias, b: BlockBuffers, stream=None):
+    def route(self, x, w_router, bias, b: BlockBuffers, stream=None, balance_bias=None):
+        if self.gate is not None:
+            api.route_gate(x, w_router, self.gate, b.logits, b.idx, b.w, b.ws_route, bias=bias,
+                           balance_bias=balance_bias, stream=stream)
+            return
+        if balance_bias is not None:
+            raise ValueError("a balance bias needs a block with a gate")
         api.route_topk(x, w_router, bias, self.k, b.logits, b.idx, b.w, stream)
 
     def permute(self, x, b: BlockBuffers, stream=None):
@@ -198,13 +217,45 @@ class MoEBlock:
     def combine(self, b: BlockBuffers, stream=None, out=None):
         api.combine(b.y_perm, b.inv_perm, b.w, self.shared, b.y if out is None else out, stream)
 
-    def forward(self, x, w_router, bias, table, stream=None, out=None) -> BlockBuffers:
+    def forward(self, x, w_router, bias, table, stream=None, out=None, balance_bias=None) -> BlockBuffers:
         """The whole block on `stream`; results stay in the returned buffers (y in `out` if given)."""
         b = self.buffers(x.shape[0])
-        self.route(x, w_router, bias, b, stream)
+        self.route(x, w_router, bias, b, stream, balance_bias)
         self.permute(x, b, stream)
         self.ffn(table, b, stream)
         self.combine(b, stream, out)
+        return b
+
+    # A pre-norm layer is h' = h + block(norm(h)).  The norm of a layer's input is written by `norm` (a
+    # model's first layer) or by the layer before it (forward_normed's next_weight), into b.x_norm and, for
+    # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.
+
+    def _norm_outputs(self, b: BlockBuffers):
+        if b.x_norm is None:
+            b.x_norm = torch.empty_like(b.y)
+        return dict(y=b.x_norm, q=b.x_q, q_scale=b.x_q_scale)
+
+    def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None):
+        """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given)."""
+        api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b))
+
+    def forward_normed(self, h, w_router, bias, table, next_weight=None, eps: float = 1e-6, stream=None, out=None,
+                       balance_bias=None) -> BlockBuffers:
+        """A layer whose normed input is in the buffers: h + block(b.x_norm) to `out` (b.y if not given; h itself
+        works), and with next_weight that sum's norm to the buffers, the next layer's input."""
+        b = self.buffers(h.shape[0])
+        if b.x_norm is None:
+            raise ValueError("no normed input: call norm() on the buffers first")
+        self.route(b.x_norm, w_router, bias, b, stream, balance_bias)
+        api.permute(b.idx, self.E, self.shared, b.x_norm,
+                    self.w_dtype if self.w_dtype == FP8_E4M3 else api.dtype_code(b.x_norm), b.x_perm, b.x_perm_scale,
+                    b.offsets, b.perm_src, b.inv_perm, b.ws_perm, stream)
+        if not self.gather:
+            b.x_tokens = b.x_norm if b.x_q is None else b.x_q
+        self.ffn(table, b, stream)
+        api.combine_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, next_weight, eps,
+                                sum_out=b.y if out is None else out, stream=stream,
+                                **(self._norm_outputs(b) if next_weight is not None else {}))
         return b
 
 
@@ -222,6 +273,9 @@ class LayerWeights:
     bias: torch.Tensor | None
     resident: torch.Tensor
     sources: list
+    balance_bias: torch.Tensor | None = None   # with a gate: steers the choice of experts
+    norm: torch.Tensor | None = None           # weight of the RMS norm before the block (None: no norm, no residual)
+    norm_eps: float = 1e-6
 
 
 class DWDPPipeline:
@@ -238,12 +292,14 @@ class DWDPPipeline:
 
     The block reads each layer's weights through a pointer table over two buffers -- the layer's
     resident records and the current slot set -- so nothing is merged.  Only the MoE blocks run here
-    (a model without attention): layer l+1's input is layer l's output.
+    (a model without attention): layer l+1's input is layer l's output.  Layers with a norm weight are
+    pre-norm residual layers, h_{l+1} = h_l + block_l(norm_l(h_l)): the first norm runs by itself, every
+    other one in the pass that combines the layer before it.
     """
 
     def __init__(self, H: int, I: int, E: int, k: int, shared: int, dtype: str, n_local: int, device="cuda",
                  slot_sets=None, chunk_bytes: int = 4 << 20, engine: int = api.COPY_KERNEL,
-                 max_workgroups: int = 48):
+                 max_workgroups: int = 48, gate: api.Gate | None = None):
         self.H, self.I, self.E, self.k, self.shared, self.n_local = H, I, E, k, shared, n_local
         self.w_dtype = DTYPES[dtype]
         self.device = torch.device(device)
@@ -256,7 +312,7 @@ class DWDPPipeline:
         assert len(slot_sets) >= 2 and all(t.numel() >= self.n_pre * self.rec for t in slot_sets)
         self.slot_sets = list(slot_sets)
         self.chunk_bytes, self.engine, self.max_workgroups = chunk_bytes, engine, max_workgroups
-        self.block = MoEBlock(H, I, E, k, shared, dtype, self.device)
+        self.block = MoEBlock(H, I, E, k, shared, dtype, self.device, gate=gate)
         self.copy_stream = torch.cuda.Stream(self.device)
         self._last_read = [None] * len(self.slot_sets)   # event of the last layer that read each slot set
         self._tables = {}
@@ -303,6 +359,11 @@ class DWDPPipeline:
         L = len(layers)
         for lw in layers:
             self.check_sources(lw)
+        normed = L > 0 and layers[0].norm is not None
+        if any((lw.norm is not None) != normed for lw in layers):
+            raise ValueError("some layers have a norm and some have none")
+        if normed and not chain:
+            raise ValueError("layers with norms are a chain")
         T = x.shape[0]
         if outputs is None:
             bufs = [torch.empty(T, self.H, dtype=x.dtype, device=self.device) for _ in range(min(L, 2))]
@@ -330,7 +391,17 @@ class DWDPPipeline:
             if before_compute is not None:
                 before_compute(l)
             lw = layers[l]
-            b = self.block.forward(x, lw.w_router, lw.bias, self.table(lw, s), out=outputs[l])
+            if normed:
+                if l == 0:
+                    self.block.norm(x, lw.norm, lw.norm_eps, self.block.buffers(T))
+                nxt = layers[l + 1] if l + 1 < L else None
+                b = self.block.forward_normed(x, lw.w_router, lw.bias, self.table(lw, s),
+                                              next_weight=None if nxt is None else nxt.norm,
+                                              eps=lw.norm_eps if nxt is None else nxt.norm_eps, out=outputs[l],
+                                              balance_bias=lw.balance_bias)
+            else:
+                b = self.block.forward(x, lw.w_router, lw.bias, self.table(lw, s), out=outputs[l],
+                                       balance_bias=lw.balance_bias)
             if after_layer is not None:
                 after_layer(l, b)
             ev = torch.cuda.Event()
