@@ -13,6 +13,10 @@ namespace dwdp {
 namespace {
 
 constexpr int kMaxK = 64;
+constexpr int kFewRows = 512;
+constexpr int kManyC = 2;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct NormArgs {
     // z's source
@@ -51,6 +55,28 @@ __device__ __forceinline__ void load_vec(const uint8_t* p, int64_t i, float* v) 
         const float4 b = *reinterpret_cast<const float4*>(p + i * 4 + 16);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
         v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+}
+
+// 16 bytes that this launch reads once.
+__device__ __forceinline__ float4 load_stream(const uint8_t* p) {
+    const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
+    return float4{v[0], v[1], v[2], v[3]};
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(const float4* raw, float* v) {
+    const float f[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
+    if constexpr (BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(__float_as_uint(f[j]) << 16);
+            v[2 * j + 1] = __uint_as_float(__float_as_uint(f[j]) & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = f[j];
+        v[4] = raw[1].x, v[5] = raw[1].y, v[6] = raw[1].z, v[7] = raw[1].w;
     }
 }
 
@@ -161,15 +187,146 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
     }
 }
 
+// ------------------------------------------------------------------------------ rows held in registers
+// A thread keeps C vectors of its row (vector c of thread i: c * blockDim.x + i) as fp32 from the one read of
+// the inputs to the one write of the outputs.  blockDim.x threads share a row; rows of one wave need no LDS
+// and are packed blockDim.y to a workgroup.  Loads past the row's end read its last vector instead, so that
+// every lane of a wave stays active up to the sum (lanes read each other's registers on the way).
+
+// Sum over the wave, the same in every lane: four exchanges inside rows of 16 lanes, then the four rows.
+__device__ __forceinline__ float wave_sum(float v) {
+#define DWDP_DPP_ADD(ctrl)                                                                                         \
+    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), ctrl, 0xf, 0xf, true))
+    DWDP_DPP_ADD(0xB1);        // lanes 1 apart
+    DWDP_DPP_ADD(0x4E);        // 2 apart
+    DWDP_DPP_ADD(0x141);       // mirrored in 8
+    DWDP_DPP_ADD(0x140);       // mirrored in 16
+#undef DWDP_DPP_ADD
+    const int b = __float_as_int(v);
+    return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
+           (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
+}
+
+template <bool COMBINE, bool BF16, int VEC, int C>
+__global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
+    __shared__ float s_part[16];
+    const int tx = threadIdx.x, bx = blockDim.x, lane = tx & 63;
+    const int n_waves = bx >> 6;
+    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += (int64_t)gridDim.x * blockDim.y) {
+        float z[C][VEC];
+        if constexpr (COMBINE) {
+            // lane j holds slot j's row and weight (k <= 64); rows out of range are dropped
+            const int64_t rows = a.T * (a.k + a.shared);
+            int my_row = -1;
+            float my_w = 0.0f;
+            if (lane < a.k) {
+                my_row = a.inv_perm[t * a.k + lane];
+                my_w = a.topk_w[t * a.k + lane];
+                if (my_row >= rows) my_row = -1;
+            }
+            const int nsrc = a.k + a.shared;
+            constexpr int B = BF16 ? 16 : 8;              // source rows whose loads are in flight together
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int col = min((c * bx + tx) * VEC, a.H - VEC);
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) z[c][u] = 0.0f;
+                for (int j0 = 0; j0 < nsrc; j0 += B) {
+                    float4 raw[B][BF16 ? 1 : 2];
+#pragma unroll
+                    for (int u = 0; u < B; ++u) {
+                        const int j = j0 + u;
+                        if (j < nsrc) {
+                            const int r = j < a.k ? __builtin_amdgcn_readlane(my_row, j) : 0;
+                            const int64_t row = j < a.k ? (r >= 0 ? r : 0) : a.T * a.k + t;
+                            const uint8_t* p = a.x + (row * a.H + col) * (BF16 ? 2 : 4);
+                            raw[u][0] = load_stream(p);
+                            if constexpr (!BF16) raw[u][1] = load_stream(p + 16);
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < B; ++u) {
+                        const int j = j0 + u;
+                        if (j >= nsrc || (j < a.k && __builtin_amdgcn_readlane(my_row, j) < 0)) continue;
+                        const float w =
+                            j < a.k ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_w), j)) : 1.0f;
+                        float v[8];
+                        unpack<BF16>(raw[u], v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) z[c][i] += w * v[i];
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                load_vec<BF16, VEC>(a.x, t * a.H + min((c * bx + tx) * VEC, a.H - VEC), z[c]);
+        }
+        if (a.residual != nullptr) {
+            float v[C][VEC];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                load_vec<BF16, VEC>(a.residual, t * a.H + min((c * bx + tx) * VEC, a.H - VEC), v[c]);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int u = 0; u < VEC; ++u) z[c][u] += v[c][u];
+        }
+        float ss = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const bool in = (c * bx + tx) * VEC < a.H;
+#pragma unroll
+            for (int u = 0; u < VEC; ++u) ss += in ? z[c][u] * z[c][u] : 0.0f;
+        }
+        ss = wave_sum(ss);
+        if (n_waves > 1) {
+            if (lane == 0) s_part[tx >> 6] = ss;
+            __syncthreads();
+            ss = 0.0f;
+            for (int i = 0; i < n_waves; ++i) ss += s_part[i];
+            __syncthreads();                          // read before the next row's sums
+        }
+        const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c * bx + tx) * VEC;
+            if (col < a.H) finish_vec<BF16, VEC>(a, t, col, z[c], r);
+        }
+    }
+}
+
+template <bool COMBINE, bool BF16, int VEC, int C>
+void launch_rows(const NormArgs& a, int threads, hipStream_t st) {
+    const int rows = threads == 64 ? 4 : 1;
+    const unsigned grid = (unsigned)std::min<int64_t>((a.T + rows - 1) / rows, kMaxRowGrid);
+    hipLaunchKernelGGL((norm_row_kernel<COMBINE, BF16, VEC, C>), dim3(grid), dim3(threads, rows), 0, st, a);
+}
+
+template <bool COMBINE, bool BF16, int VEC>
+void launch_typed(const NormArgs& a, hipStream_t st) {
+    // the largest counts that stay in 128 registers (combine: its source rows in flight take the rest)
+    constexpr int C1 = VEC == 8 ? kManyC : 4, C2 = COMBINE ? C1 : VEC == 8 ? 4 : 8;
+    const int64_t nvec = (a.H + VEC - 1) / VEC;
+    auto threads = [&](int c) { return (int)(((nvec + c - 1) / c + 63) / 64 * 64); };
+    if (threads(1) <= 64 || (a.T <= kFewRows && threads(1) <= 1024))
+        launch_rows<COMBINE, BF16, VEC, 1>(a, threads(1), st);
+    else if (threads(C1) <= 1024) launch_rows<COMBINE, BF16, VEC, C1>(a, threads(C1), st);
+    else if (C2 != C1 && threads(C2) <= 1024) launch_rows<COMBINE, BF16, VEC, C2>(a, threads(C2), st);
+    else {
+        const dim3 grid((unsigned)std::min<int64_t>(a.T, kMaxRowGrid));
+        hipLaunchKernelGGL((norm_two_pass_kernel<COMBINE, BF16, VEC>), grid, dim3(256), 0, st, a);
+    }
+}
+
 template <bool COMBINE>
 int launch_norm(const NormArgs& a, bool bf16, bool vec, hipStream_t st) {
-    const dim3 grid((unsigned)std::min<int64_t>(a.T, kMaxRowGrid)), block(256);
     if (vec) {
-        if (bf16) hipLaunchKernelGGL((norm_two_pass_kernel<COMBINE, true, 8>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((norm_two_pass_kernel<COMBINE, false, 8>), grid, block, 0, st, a);
+        if (bf16) launch_typed<COMBINE, true, 8>(a, st);
+        else launch_typed<COMBINE, false, 8>(a, st);
     } else if constexpr (!COMBINE) {
-        if (bf16) hipLaunchKernelGGL((norm_two_pass_kernel<false, true, 1>), grid, block, 0, st, a);
-        else hipLaunchKernelGGL((norm_two_pass_kernel<false, false, 1>), grid, block, 0, st, a);
+        if (bf16) launch_typed<false, true, 1>(a, st);
+        else launch_typed<false, false, 1>(a, st);
     }
     DWDP_LAUNCHED();
     return DWDP_OK;
