@@ -215,27 +215,31 @@ class Gate:
         object.__setattr__(self, "_c", c)
 
 
-def _check(name, t, shape, dtypes, device):
-    """t's address, or None for None; ValueError unless t is a dense tensor of that shape, type and device."""
+def _check(name, t, shape, dtypes, index):
+    """t's address, or None for None; ValueError unless t is a dense tensor of that shape, type and GPU."""
     if t is None:
         return None
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.get_device() == index:
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be of type {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be dense and row-major (contiguous)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on GPU {index}")
 
 
-def _check_device(name, t):
-    """t's device, which must be the current GPU: streams and launches belong to it."""
-    d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {d}, which is not the current GPU")
-    return d
+def _gpu_index(name, t):
+    """The number of t's GPU, which must be the current one: streams and launches belong to it."""
+    i = t.get_device()
+    if i < 0 or i != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, which is not the current GPU")
+    return i
+
+
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _matrix(name, t):
@@ -257,7 +261,7 @@ def route_gate_workspace_bytes(T: int, H: int, E: int, dtype: int) -> int:
 def route_gate(x, w_router, gate, logits_out, topk_idx, topk_w, ws=None, bias=None, balance_bias=None, stream=None):
     """Router product and gate: x [T, H], w_router [E, H] -> logits_out [T, E], topk_idx, topk_w [T, k]."""
     (T, H), E = _matrix("x", x), _matrix("w_router", w_router)[0]
-    dev = _check_device("x", x)
+    dev = _gpu_index("x", x)
     px = _check("x", x, (T, H), _ACT, dev)
     pw = _check("w_router", w_router, (E, H), (x.dtype,), dev)
     pl = _check("logits_out", logits_out, (T, E), _F32, dev)
@@ -269,25 +273,25 @@ def route_gate(x, w_router, gate, logits_out, topk_idx, topk_w, ws=None, bias=No
     if ws is not None:
         nws = ws.numel() * ws.element_size()
         pws = _check("ws", ws, ws.shape, (ws.dtype,), dev)
-    _lib.check(_lib.load().dwdp_route_gate(px, pw, dtype_code(x), pb, pbb, T, H, E, ctypes.byref(gate._c), pl, pi, pt,
-                                           pws, nws, _stream(stream)))
+    _lib.check(_lib.load().dwdp_route_gate(px, pw, _DT[x.dtype], pb, pbb, T, H, E, ctypes.byref(gate._c), pl, pi, pt,
+                                           pws, nws, _raw_stream(stream, dev)))
 
 
 def gate_topk(logits, gate, topk_idx, topk_w, balance_bias=None, stream=None):
     """The gate alone: logits [T, E] -> topk_idx, topk_w [T, k]."""
     T, E = _matrix("logits", logits)
-    dev = _check_device("logits", logits)
+    dev = _gpu_index("logits", logits)
     pl = _check("logits", logits, (T, E), _F32, dev)
     pi = _check("topk_idx", topk_idx, (T, gate.k), _I32, dev)
     pt = _check("topk_w", topk_w, (T, gate.k), _F32, dev)
     pbb = _check("balance_bias", balance_bias, (E,), _F32, dev)
-    _lib.check(_lib.load().dwdp_gate_topk(pl, pbb, T, E, ctypes.byref(gate._c), pi, pt, _stream(stream)))
+    _lib.check(_lib.load().dwdp_gate_topk(pl, pbb, T, E, ctypes.byref(gate._c), pi, pt, _raw_stream(stream, dev)))
 
 
 def _norm_outputs(T, H, act, dev, residual, weight, sum_out, y, q, q_scale):
     act = (act,)
     return (_check("residual", residual, (T, H), act, dev), _check("weight", weight, (H,), _ACT, dev),
-            F32 if weight is None else dtype_code(weight), _check("sum_out", sum_out, (T, H), act, dev),
+            F32 if weight is None else _DT[weight.dtype], _check("sum_out", sum_out, (T, H), act, dev),
             _check("y", y, (T, H), act, dev), _check("q", q, (T, H), _U8, dev),
             _check("q_scale", q_scale, (T, H // 128), _F32, dev))
 
@@ -295,11 +299,11 @@ def _norm_outputs(T, H, act, dev, residual, weight, sum_out, y, q, q_scale):
 def add_rmsnorm(x, residual, weight, eps, sum_out=None, y=None, q=None, q_scale=None, stream=None):
     """z = x + residual; sum_out = z, y = z / rms(z) * weight, (q, q_scale) = y's E4M3 codes and 1x128 scales."""
     T, H = _matrix("x", x)
-    dev = _check_device("x", x)
+    dev = _gpu_index("x", x)
     px = _check("x", x, (T, H), _ACT, dev)
     pr, pw, wd, ps, py, pq, pqs = _norm_outputs(T, H, x.dtype, dev, residual, weight, sum_out, y, q, q_scale)
-    _lib.check(_lib.load().dwdp_add_rmsnorm(px, pr, dtype_code(x), pw, wd, eps, T, H, ps, py, pq, pqs,
-                                            _stream(stream)))
+    _lib.check(_lib.load().dwdp_add_rmsnorm(px, pr, _DT[x.dtype], pw, wd, eps, T, H, ps, py, pq, pqs,
+                                            _raw_stream(stream, dev)))
 
 
 def combine_add_rmsnorm(y_perm, inv_perm, topk_w, shared, residual, weight, eps, sum_out=None, y=None, q=None,
@@ -307,13 +311,13 @@ def combine_add_rmsnorm(y_perm, inv_perm, topk_w, shared, residual, weight, eps,
     """The layer boundary: z = combine(y_perm) + residual; outputs as in add_rmsnorm (weight None: sum_out alone)."""
     T, k = _matrix("inv_perm", inv_perm)
     H = _matrix("y_perm", y_perm)[1]
-    dev = _check_device("y_perm", y_perm)
+    dev = _gpu_index("y_perm", y_perm)
     px = _check("y_perm", y_perm, (T * (k + shared), H), _ACT, dev)
     pi = _check("inv_perm", inv_perm, (T, k), _I32, dev)
     pt = _check("topk_w", topk_w, (T, k), _F32, dev)
     pr, pw, wd, ps, py, pq, pqs = _norm_outputs(T, H, y_perm.dtype, dev, residual, weight, sum_out, y, q, q_scale)
-    _lib.check(_lib.load().dwdp_combine_add_rmsnorm(px, pi, pt, T, k, shared, H, dtype_code(y_perm), pr, pw, wd, eps, ps,
-                                                    py, pq, pqs, _stream(stream)))
+    _lib.check(_lib.load().dwdp_combine_add_rmsnorm(px, pi, pt, T, k, shared, H, _DT[y_perm.dtype], pr, pw, wd, eps, ps,
+                                                    py, pq, pqs, _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------------------------ diagnostics (not steps of the block)

@@ -19,7 +19,7 @@ constexpr int kMaxK = 32;
 constexpr int kNone = 0x7fffffff;     // no expert
 
 struct GateArgs {
-    const float* logits;
+    const float* logits;              // [T,E] (split kernel: written by it, bias included)
     const float* balance;             // [E] or null
     int64_t T;
     int E, k, groups, kept, group_top;
@@ -27,6 +27,8 @@ struct GateArgs {
     float scale;
     int32_t* idx;
     float* w;
+    // lane layout of gate_lanes_kernel: a group is group_lanes lanes (a power of two) of per_lane experts
+    int group_lanes, per_lane;
 };
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -177,6 +179,217 @@ __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
         gate_row_exact<PL>(a, t, c);
 }
 
+// ------------------------------------------------------------------------------ tokens side by side
+// L lanes per token (16 of them, so that a wave takes four tokens and reductions stay in a row of 16 lanes;
+// or 64), up to PL consecutive experts per lane, in expert order.  Keys are fp32: the logits themselves
+// without a balance bias (their order is exact), else score + bias from the hardware exponential and
+// reciprocal.  Those carry an error, so every decision taken on them is checked: where two consecutive
+// picks, or the last group kept and the first one dropped, are closer than twice the error bound, the wave
+// repeats the token in fp64 (gate_row_exact).  The choice therefore is the fp64 one in every case, and one
+// token in about a thousand of ordinary logits pays for it.
+//
+// Error bounds (u = 2^-24).  exp2 and rcp have errors of 2 u, products and sums 1 u.
+//   sigmoid: s = 1 / (1 + e), e = exp2(-l log2e): the exponent's error enters e relative by 1.5 |l| u, so s is
+//     off by at most s (1 - s) (1.5 |l| + 2) u + 3 s u <= 3.9 u, since s (1 - s) |l| <= 0.23.
+//   softmax: f = exp2((l - m) log2e) / S with S >= 1: the numerator is off by at most 3 u, S by 42 u relative
+//     (the mean of |l - m| under the softmax is at most ln 1024), so s by at most 51 u / S, as s <= 1 / S.
+//   the bias' addition adds u |c|.
+// Two keys: twice that.  kTol* below are those sums rounded up to powers of two.
+constexpr float kTolSigmoid = 0x1p-20f;       // >= 2 * 3.9 u
+constexpr float kTolSoftmax = 0x1p-17f;       // >= 2 * 51 u, times 1 / S
+constexpr float kTolChoice = 0x1p-22f;        // >= 2 u, times the key
+
+__device__ __forceinline__ float f_neg_inf() { return -__builtin_huge_valf(); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+
+struct MaxOp {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct MinOp {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
+};
+struct AddOp {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// Over the L lanes of a token, the same in each of them.
+template <int L, class Op>
+__device__ __forceinline__ float over_token(float v, Op op) {
+    v = op(v, dpp<0xB1>(v));                  // lanes 1 apart
+    v = op(v, dpp<0x4E>(v));                  // 2 apart
+    v = op(v, dpp<0x141>(v));                 // mirrored in 8
+    v = op(v, dpp<0x140>(v));                 // mirrored in 16
+    if constexpr (L == 64) {
+        const int b = __float_as_int(v);
+        v = op(op(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __int_as_float(__builtin_amdgcn_readlane(b, 16))),
+               op(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
+    }
+    return v;
+}
+
+// First lane of this lane's token whose bit is set (its number in the token); none set: 32 or more.
+template <int L>
+__device__ __forceinline__ int first_lane(unsigned long long b) {
+    if constexpr (L == 64) return b == 0 ? 64 : __builtin_ctzll(b);
+    const int lane = threadIdx.x & 63;
+    const uint32_t half = lane < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
+    const uint32_t seg = (half >> (lane & 16)) & 0xffffu;
+    return __builtin_ctz(seg | 0x80000000u);
+}
+
+template <int L, int PL>
+__global__ __launch_bounds__(256) void gate_lanes_kernel(GateArgs a) {
+    constexpr int TPW = 64 / L;                       // tokens per wave
+    constexpr int XPL = L == 16 ? 4 : PL;             // experts per lane of the fp64 form (64 lanes)
+    extern __shared__ double lds[];
+    __shared__ int s_slot[4][TPW][L < kMaxK ? L : kMaxK];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & (L - 1), tok = lane / L;
+    double* xc = lds + wave * (a.E + a.groups);       // only laid out where groups > 1
+    const int gs = a.E / a.groups, g = q / a.group_lanes;
+    const int in_group = (q & (a.group_lanes - 1)) * a.per_lane;
+    const int base = g * gs + in_group;
+    const int count = g < a.groups ? max(0, min(a.per_lane, gs - in_group)) : 0;
+    const bool biased = a.balance != nullptr;
+    const bool pairs = a.groups > 1 && a.group_top == 2;
+    const bool need_scores = biased || pairs;
+    const bool vec = (a.per_lane & 3) == 0 && (gs & 3) == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW; t0 < a.T; t0 += (int64_t)gridDim.x * 4 * TPW) {
+        const int64_t t = min(t0 + tok, a.T - 1);     // lanes behind the last token repeat it and write nothing
+        const float* row = a.logits + t * a.E + base;
+        float l[PL], v[PL];
+        if (vec) {                                    // counts are multiples of 4 too
+#pragma unroll
+            for (int i = 0; i < PL; i += 4) {
+                float4 x = float4{f_neg_inf(), f_neg_inf(), f_neg_inf(), f_neg_inf()};
+                if (i < count) x = *reinterpret_cast<const float4*>(row + i);
+                l[i] = x.x, l[i + 1] = x.y, l[i + 2] = x.z, l[i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) l[i] = i < count ? row[i] : f_neg_inf();
+        }
+        // NaN counts as -inf; adding 0 makes -0 into +0
+        float m = f_neg_inf();
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            l[i] = l[i] > f_neg_inf() ? l[i] + 0.0f : f_neg_inf();
+            m = fmaxf(m, l[i]);
+        }
+        constexpr float kLog2e = 1.44269504088896340736f;
+        float sum = 1.0f, tol = kTolSigmoid;
+        if (!a.sigmoid && (need_scores || !a.renorm)) {
+            m = over_token<L>(m, MaxOp());
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                v[i] = l[i] == m ? 1.0f : __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
+                v[i] = l[i] > f_neg_inf() ? v[i] : 0.0f;
+                sum += v[i];
+            }
+            sum = over_token<L>(sum, AddOp());
+            const float inv = __builtin_amdgcn_rcpf(sum);
+            tol = kTolSoftmax * inv;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) v[i] *= inv;
+        } else if (need_scores) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                v[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
+        }
+        bool unsure = false;
+        if (biased) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const float b = i < count ? a.balance[base + i] : f_neg_inf();
+                v[i] = l[i] > f_neg_inf() && live_logit(b) ? v[i] + b : f_neg_inf();
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) v[i] = pairs && l[i] > f_neg_inf() ? v[i] : l[i];
+        }
+        if (a.groups > 1) {
+            float b1 = f_neg_inf(), b2 = f_neg_inf();
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                b2 = fmaxf(b2, fminf(b1, v[i]));
+                b1 = fmaxf(b1, v[i]);
+            }
+            for (int d = 1; d < a.group_lanes; d <<= 1) {
+                const float o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+                b1 = fmaxf(b1, o1);
+            }
+            const float value = pairs && b2 > f_neg_inf() ? b1 + b2 : b1;
+            int before = 0;
+            for (int h = 0; h < a.groups; ++h) {
+                const float o = __shfl(value, h * a.group_lanes, L);
+                before += o > value || (o == value && h < g);
+            }
+            const bool kept = before < a.kept && g < a.groups;
+            if (need_scores) {                        // fp32 scores: is the border wide enough?
+                const float lo = over_token<L>(kept ? value : -f_neg_inf(), MinOp());
+                const float hi = over_token<L>(!kept && g < a.groups ? value : f_neg_inf(), MaxOp());
+                unsure |= hi > f_neg_inf() && !(lo - hi >= 2.0f * tol + 2.0f * kTolChoice * fabsf(lo));
+            }
+#pragma unroll
+            for (int i = 0; i < PL; ++i) v[i] = !kept ? f_neg_inf() : biased ? v[i] : l[i];
+        }
+        float prev = 0.0f;
+        int slots = 0;                                // slots filled
+        for (int j = 0; j <= a.k; ++j) {
+            if (j == a.k && !biased) break;           // the pick behind the last only matters to the check
+            float best = v[0];
+#pragma unroll
+            for (int i = 1; i < PL; ++i) best = fmaxf(best, v[i]);
+            const float top = over_token<L>(best, MaxOp());
+            const bool some = top > f_neg_inf();
+            if (biased && j > 0)
+                unsure |= some && !(prev - top >= tol + kTolChoice * fabsf(prev));
+            prev = top;
+            if (j == a.k) break;
+            bool take = some && first_lane<L>(__ballot(best == top)) == q;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) {
+                const bool hit = take && v[i] == top;
+                v[i] = hit ? f_neg_inf() : v[i];
+                if (hit) s_slot[wave][tok][j] = base + i;
+                take = take && !hit;
+            }
+            slots += some;
+        }
+        wave_lds_sync();
+        // weights: lane j of the token has slot j
+        const bool has = q < slots;
+        const int my_i = has ? s_slot[wave][tok][q] : 0;
+        const float x = has ? a.logits[t * a.E + my_i] : 0.0f;
+        float num = 0.0f;
+        if (a.renorm) {
+            const float f = a.sigmoid ? fminf(x, 0.0f) : x;
+            const float fm = over_token<L>(has ? f : f_neg_inf(), MaxOp());
+            num = !has ? 0.0f : (f == fm ? 1.0f : expf(f - fm)) / (a.sigmoid ? 1.0f + expf(-fabsf(x)) : 1.0f);
+            const float tot = over_token<L>(num, AddOp());
+            num = has ? num / tot : 0.0f;
+        } else if (has) {
+            num = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : (x == m ? 1.0f : expf(x - m)) / sum;
+        }
+        const unsigned long long redo = __ballot(unsure);
+        const bool mine = ((redo >> (lane & ~(L - 1))) & 1) == 0;
+        if (q < a.k && t0 + tok < a.T && mine) {
+            a.idx[t * a.k + q] = has ? my_i : -1;
+            a.w[t * a.k + q] = num * a.scale;
+        }
+        if (redo != 0) {
+            for (int i = 0; i < TPW; ++i)
+                if (((redo >> (i * L)) & 1) != 0 && t0 + i < a.T) gate_row_exact<XPL>(a, t0 + i, xc);
+        }
+        wave_lds_sync();                              // s_slot is read before the next token's picks
+    }
+}
+
 bool aligned4(const void* a, const void* b, const void* c, const void* d, const void* e = nullptr) {
     return type_aligned(a, 4) && type_aligned(b, 4) && type_aligned(c, 4) && type_aligned(d, 4) && type_aligned(e, 4);
 }
@@ -221,14 +434,40 @@ GateArgs gate_args(const float* logits, const float* balance, int64_t T, int E, 
     return a;
 }
 
-int launch_gate(const GateArgs& a, hipStream_t st) {
+template <int L, int PL>
+bool launch_lanes(GateArgs& a, hipStream_t st) {
+    // a group on the fewest lanes (a power of two) that hold it; without groups, the whole token
+    const int gs = a.E / a.groups;
+    int lanes = a.groups == 1 ? L : 1;
+    while (lanes < L && (gs + lanes - 1) / lanes > PL) lanes *= 2;
+    int per = (gs + lanes - 1) / lanes;
+    if (per > PL || lanes * a.groups > L || a.k > L) return false;
+    if (gs % 4 == 0) per = (per + 3) / 4 * 4;         // 16-byte loads
+    a.group_lanes = lanes;
+    a.per_lane = per;
+    const int64_t waves = (a.T + 64 / L - 1) / (64 / L);
+    const dim3 grid((unsigned)std::min<int64_t>((waves + 3) / 4, kMaxRowGrid));
+    const size_t lds = a.groups > 1 ? 4 * (size_t)(a.E + a.groups) * sizeof(double) : 0;   // for gate_row_exact
+    hipLaunchKernelGGL((gate_lanes_kernel<L, PL>), grid, dim3(256), lds, st, a);
+    return true;
+}
+
+template <int PL>
+void launch_exact(const GateArgs& a, hipStream_t st) {
     const dim3 grid((unsigned)std::min<int64_t>((a.T + 3) / 4, kMaxRowGrid));
     const size_t lds = a.groups > 1 ? 4 * (size_t)(a.E + a.groups) * sizeof(double) : 0;   // at most 64 KB
-    if (a.E <= 64) hipLaunchKernelGGL(gate_exact_kernel<1>, grid, dim3(256), lds, st, a);
-    else if (a.E <= 128) hipLaunchKernelGGL(gate_exact_kernel<2>, grid, dim3(256), lds, st, a);
-    else if (a.E <= 256) hipLaunchKernelGGL(gate_exact_kernel<4>, grid, dim3(256), lds, st, a);
-    else if (a.E <= 512) hipLaunchKernelGGL(gate_exact_kernel<8>, grid, dim3(256), lds, st, a);
-    else hipLaunchKernelGGL(gate_exact_kernel<16>, grid, dim3(256), lds, st, a);
+    hipLaunchKernelGGL(gate_exact_kernel<PL>, grid, dim3(256), lds, st, a);
+}
+
+int launch_gate(GateArgs a, hipStream_t st) {
+    // the lane layouts that hold the gate, the narrowest first; else (more groups than lanes) one wave per token
+    // in fp64 throughout
+    if (!((a.E <= 256 && (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
+          (a.E <= 512 && launch_lanes<64, 8>(a, st)) || launch_lanes<64, 16>(a, st))) {
+        if (a.E <= 256) launch_exact<4>(a, st);
+        else if (a.E <= 512) launch_exact<8>(a, st);
+        else launch_exact<16>(a, st);
+    }
     DWDP_LAUNCHED();
     return DWDP_OK;
 }

@@ -192,16 +192,18 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu():
 def test_tensor_checks():
     """The check every tensor of these calls goes through (on CPU tensors: it reads no device memory)."""
     from split_weight_expert_amd import api
-    cpu = torch.device("cpu")
+    cpu = -1                                   # a CPU tensor's device number
     f32 = (torch.float32,)
     t = torch.zeros(4, 8)
     assert api._check("t", None, (4, 8), f32, cpu) is None
     assert api._check("t", t, (4, 8), f32, cpu) == t.data_ptr()
     for bad, match in ((torch.zeros(4, 9), "shape"), (torch.zeros(4, 8, dtype=torch.float64), "type"),
                        (torch.zeros(8, 4).t(), "dense"), (torch.zeros(4, 16)[:, ::2], "dense"),
-                       (torch.zeros(4, 8, device="meta"), "is on")):
+                       ):
         with pytest.raises(ValueError, match=match):
             api._check("t", bad, (4, 8), f32, cpu)
+    with pytest.raises(ValueError, match="is on cpu, not on GPU 0"):
+        api._check("t", t, (4, 8), f32, 0)
 
 
 def test_pipeline_refuses_mixed_norms():
