@@ -17,6 +17,13 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr int kNone = 0x7fffffff;     // no expert
+#ifndef GLB
+#define GLB 2
+#endif
+#ifndef FEW
+#define FEW 2048
+#endif
+constexpr int64_t kFewTokens = FEW;
 
 struct GateArgs {
     const float* logits;              // [T,E] (split kernel: written by it, bias included)
@@ -180,13 +187,21 @@ __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
 }
 
 // ------------------------------------------------------------------------------ tokens side by side
-// L lanes per token (16 of them, so that a wave takes four tokens and reductions stay in a row of 16 lanes;
-// or 64), up to PL consecutive experts per lane, in expert order.  Keys are fp32: the logits themselves
-// without a balance bias (their order is exact), else score + bias from the hardware exponential and
-// reciprocal.  Those carry an error, so every decision taken on them is checked: where two consecutive
-// picks, or the last group kept and the first one dropped, are closer than twice the error bound, the wave
-// repeats the token in fp64 (gate_row_exact).  The choice therefore is the fp64 one in every case, and one
-// token in about a thousand of ordinary logits pays for it.
+// L lanes per token (16: a wave takes four tokens and reductions stay in a row of 16 lanes; or 64), up to PL
+// consecutive experts per lane, in expert order.
+//
+// Keys.  An expert's key is an fp64 number: its choice with the low 10 mantissa bits replaced by the expert's
+// number (reversed for positive values), so that keys are unique, the larger key is the better choice, equal
+// choices go to the lower expert, and the maximum alone says who won: a round of the top-k is a maximum over
+// the token and a comparison per expert, with no search for the winner.  fp64 maxima and comparisons issue at
+// the rate of fp32 ones here.
+//
+// Precision.  Without a balance bias keys are the fp32 logits, exact.  Else they are choices from the
+// hardware's fp32 exponential and reciprocal, and every decision on them is checked against the error bounds
+// below.  Where the last group kept and the first one dropped are too close, the groups are ranked again by
+// the fp64 choices of their two best; where two consecutive picks are, the k picks and the next best, one per
+// lane, by theirs (one token in some hundreds of ordinary logits).  Where another expert is so close that it
+// could have taken part, gate_row_exact repeats the token.  So the choice is the fp64 one in every case.
 //
 // Error bounds (u = 2^-24).  exp2 and rcp have errors of 2 u, products and sums 1 u.
 //   sigmoid: s = 1 / (1 + e), e = exp2(-l log2e): the exponent's error enters e relative by 1.5 |l| u, so s is
@@ -194,59 +209,91 @@ __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
 //   softmax: f = exp2((l - m) log2e) / S with S >= 1: the numerator is off by at most 3 u, S by 42 u relative
 //     (the mean of |l - m| under the softmax is at most ln 1024), so s by at most 51 u / S, as s <= 1 / S.
 //   the bias' addition adds u |c|.
-// Two keys: twice that.  kTol* below are those sums rounded up to powers of two.
-constexpr float kTolSigmoid = 0x1p-20f;       // >= 2 * 3.9 u
+// Two keys: twice that.  kTol* are those sums rounded up to powers of two.
+constexpr float kTolSigmoid = 0x1p-21f;       // >= 2 * 3.9 u
 constexpr float kTolSoftmax = 0x1p-17f;       // >= 2 * 51 u, times 1 / S
 constexpr float kTolChoice = 0x1p-22f;        // >= 2 u, times the key
 
+constexpr uint32_t kKeyMask = 1023;           // expert numbers: E <= 1024
+constexpr uint32_t kGoneHi = 0xffefffffu;     // high word of a key that cannot be (or was) chosen: below -2^1023
+constexpr uint32_t kInfHi = 0x7e700000u;      // high word of the key of a choice of +inf: 2^1000
+
 __device__ __forceinline__ float f_neg_inf() { return -__builtin_huge_valf(); }
+__device__ __forceinline__ uint32_t hi32(double v) { return (uint32_t)(__double_as_longlong(v) >> 32); }
+__device__ __forceinline__ uint32_t lo32(double v) { return (uint32_t)__double_as_longlong(v); }
+__device__ __forceinline__ double from32(uint32_t hi, uint32_t lo) {
+    return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
+}
+__device__ __forceinline__ bool gone(double key) { return key < -0x1p1022; }
+
+// Maximum of two numbers that are no NaN (the compiler's fmax would first quiet each operand).
+__device__ __forceinline__ double max64(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+__device__ __forceinline__ double min64(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+// c as the key of expert e.  c: no NaN; -inf cannot be chosen.
+__device__ __forceinline__ double make_key(double c, int e) {
+    const uint32_t h = hi32(c), s = (uint32_t)((int32_t)h >> 31);
+    const uint32_t lo = (lo32(c) & ~kKeyMask) | ((s ^ (uint32_t)~e) & kKeyMask);
+    return from32(h == 0xfff00000u ? kGoneHi : h == 0x7ff00000u ? kInfHi : h, lo);
+}
+__device__ __forceinline__ int key_expert(double key) {
+    const uint32_t s = (uint32_t)((int32_t)hi32(key) >> 31);
+    return (int)((lo32(key) ^ ~s) & kKeyMask);
+}
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
-
-struct MaxOp {
-    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct MinOp {
-    __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
-};
-struct AddOp {
-    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    return from32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi32(v), CTRL, 0xf, 0xf, true),
+                  (uint32_t)__builtin_amdgcn_update_dpp(0, (int)lo32(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float read_lane(float v, int l) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ double read_lane(double v, int l) {
+    return from32((uint32_t)__builtin_amdgcn_readlane((int)hi32(v), l), (uint32_t)__builtin_amdgcn_readlane((int)lo32(v), l));
+}
 
 // Over the L lanes of a token, the same in each of them.
-template <int L, class Op>
-__device__ __forceinline__ float over_token(float v, Op op) {
+template <int L, class V, class Op>
+__device__ __forceinline__ V over_token(V v, Op op) {
     v = op(v, dpp<0xB1>(v));                  // lanes 1 apart
     v = op(v, dpp<0x4E>(v));                  // 2 apart
     v = op(v, dpp<0x141>(v));                 // mirrored in 8
     v = op(v, dpp<0x140>(v));                 // mirrored in 16
-    if constexpr (L == 64) {
-        const int b = __float_as_int(v);
-        v = op(op(__int_as_float(__builtin_amdgcn_readlane(b, 0)), __int_as_float(__builtin_amdgcn_readlane(b, 16))),
-               op(__int_as_float(__builtin_amdgcn_readlane(b, 32)), __int_as_float(__builtin_amdgcn_readlane(b, 48))));
-    }
+    if constexpr (L == 64) v = op(op(read_lane(v, 0), read_lane(v, 16)), op(read_lane(v, 32), read_lane(v, 48)));
     return v;
 }
-
-// First lane of this lane's token whose bit is set (its number in the token); none set: 32 or more.
-template <int L>
-__device__ __forceinline__ int first_lane(unsigned long long b) {
-    if constexpr (L == 64) return b == 0 ? 64 : __builtin_ctzll(b);
-    const int lane = threadIdx.x & 63;
-    const uint32_t half = lane < 32 ? (uint32_t)b : (uint32_t)(b >> 32);
-    const uint32_t seg = (half >> (lane & 16)) & 0xffffu;
-    return __builtin_ctz(seg | 0x80000000u);
-}
+struct MaxF {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct AddF {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct AddD {
+    __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
+};
+struct MaxKey {
+    __device__ __forceinline__ double operator()(double a, double b) const { return max64(a, b); }
+};
 
 template <int L, int PL>
-__global__ __launch_bounds__(256) void gate_lanes_kernel(GateArgs a) {
+__global__ __launch_bounds__(256, GLB) void gate_lanes_kernel(GateArgs a) {
     constexpr int TPW = 64 / L;                       // tokens per wave
-    constexpr int XPL = L == 16 ? 4 : PL;             // experts per lane of the fp64 form (64 lanes)
+    constexpr int XPL = L * PL <= 256 ? 4 : PL;       // experts per lane of gate_row_exact (64 lanes)
     extern __shared__ double lds[];
-    __shared__ int s_slot[4][TPW][L < kMaxK ? L : kMaxK];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & (L - 1), tok = lane / L;
     double* xc = lds + wave * (a.E + a.groups);       // only laid out where groups > 1
     const int gs = a.E / a.groups, g = q / a.group_lanes;
@@ -255,138 +302,196 @@ __global__ __launch_bounds__(256) void gate_lanes_kernel(GateArgs a) {
     const int count = g < a.groups ? max(0, min(a.per_lane, gs - in_group)) : 0;
     const bool biased = a.balance != nullptr;
     const bool pairs = a.groups > 1 && a.group_top == 2;
-    const bool need_scores = biased || pairs;
-    const bool vec = (a.per_lane & 3) == 0 && (gs & 3) == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0;
-    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW; t0 < a.T; t0 += (int64_t)gridDim.x * 4 * TPW) {
-        const int64_t t = min(t0 + tok, a.T - 1);     // lanes behind the last token repeat it and write nothing
-        const float* row = a.logits + t * a.E + base;
-        float l[PL], v[PL];
-        if (vec) {                                    // counts are multiples of 4 too
+    const bool need_scores = biased || pairs;         // keys, or groups' values, from inexact scores
+    const bool vec = (a.per_lane & 3) == 0 && (gs & 3) == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.balance) & 15) == 0;
+    // PL consecutive floats of this lane, -inf behind its count (with vec, counts are multiples of 4 too)
+    auto load = [&](const float* p, float* x) {
+        if (vec) {
 #pragma unroll
             for (int i = 0; i < PL; i += 4) {
-                float4 x = float4{f_neg_inf(), f_neg_inf(), f_neg_inf(), f_neg_inf()};
-                if (i < count) x = *reinterpret_cast<const float4*>(row + i);
-                l[i] = x.x, l[i + 1] = x.y, l[i + 2] = x.z, l[i + 3] = x.w;
+                float4 r = float4{f_neg_inf(), f_neg_inf(), f_neg_inf(), f_neg_inf()};
+                if (i < count) r = *reinterpret_cast<const float4*>(p + i);
+                x[i] = r.x, x[i + 1] = r.y, x[i + 2] = r.z, x[i + 3] = r.w;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < PL; ++i) l[i] = i < count ? row[i] : f_neg_inf();
+            for (int i = 0; i < PL; ++i) x[i] = i < count ? p[i] : f_neg_inf();
         }
-        // NaN counts as -inf; adding 0 makes -0 into +0
+    };
+    constexpr unsigned long long kToken = L == 64 ? ~0ull : (1ull << (L & 63)) - 1;
+    // The softmax's denominator and an expert's choice in fp64, for close calls.  m: the largest logit.
+    auto softmax_total = [&](int64_t t, float m) {
+        double s = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < PL; ++i) {                // rolled: rare, and registers are dear
+            const float x = i < count ? a.logits[t * a.E + base + i] : f_neg_inf();
+            if (x > f_neg_inf()) s += x == m ? 1.0 : exp((double)x - (double)m);
+        }
+        return over_token<L>(s, AddD());
+    };
+    auto choice64 = [&](int64_t t, int e, float m, double total) {
+        const float x = a.logits[t * a.E + e];
+        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : (x == m ? 1.0 : exp((double)x - (double)m)) / total;
+        return biased ? s + (double)a.balance[e] : s;
+    };
+    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW; t0 < a.T; t0 += (int64_t)gridDim.x * 4 * TPW) {
+        const int64_t t = min(t0 + tok, a.T - 1);     // lanes behind the last token repeat it and write nothing
+        float l[PL], b[PL];
+        load(a.logits + t * a.E + base, l);
+        if (biased) load(a.balance + base, b);
         float m = f_neg_inf();
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
+            // NaN counts as -inf; adding 0 makes -0 into +0.  An expert without a live bias is out, but its logit
+            // stays in the softmax.
             l[i] = l[i] > f_neg_inf() ? l[i] + 0.0f : f_neg_inf();
+            if (biased) b[i] = l[i] > f_neg_inf() && b[i] > f_neg_inf() ? b[i] : f_neg_inf();
             m = fmaxf(m, l[i]);
         }
         constexpr float kLog2e = 1.44269504088896340736f;
-        float sum = 1.0f, tol = kTolSigmoid;
-        if (!a.sigmoid && (need_scores || !a.renorm)) {
-            m = over_token<L>(m, MaxOp());
-            sum = 0.0f;
+        float sum = 1.0f;                             // the softmax's denominator in units of exp(m)
+        float tol = kTolSigmoid;
+        double key[PL];
+        {
+            float s[PL];
+            if (!a.sigmoid && (need_scores || !a.renorm)) {
+                m = over_token<L>(m, MaxF());
+                sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    s[i] = l[i] == m ? 1.0f : __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
+                    s[i] = l[i] > f_neg_inf() ? s[i] : 0.0f;
+                    sum += s[i];
+                }
+                sum = over_token<L>(sum, AddF());
+                const float inv = __builtin_amdgcn_rcpf(sum);
+                tol = kTolSoftmax * inv;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) s[i] *= inv;
+            } else if (need_scores) {
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    s[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
+            }
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
-                v[i] = l[i] == m ? 1.0f : __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
-                v[i] = l[i] > f_neg_inf() ? v[i] : 0.0f;
-                sum += v[i];
+                float c = l[i];
+                if (biased) c = b[i] > f_neg_inf() ? s[i] + b[i] : f_neg_inf();
+                else if (pairs) c = l[i] > f_neg_inf() ? s[i] : f_neg_inf();
+                key[i] = make_key((double)c, base + i);
             }
-            sum = over_token<L>(sum, AddOp());
-            const float inv = __builtin_amdgcn_rcpf(sum);
-            tol = kTolSoftmax * inv;
-#pragma unroll
-            for (int i = 0; i < PL; ++i) v[i] *= inv;
-        } else if (need_scores) {
-#pragma unroll
-            for (int i = 0; i < PL; ++i)
-                v[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
         }
         bool unsure = false;
-        if (biased) {
-#pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                const float b = i < count ? a.balance[base + i] : f_neg_inf();
-                v[i] = l[i] > f_neg_inf() && live_logit(b) ? v[i] + b : f_neg_inf();
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < PL; ++i) v[i] = pairs && l[i] > f_neg_inf() ? v[i] : l[i];
-        }
         if (a.groups > 1) {
-            float b1 = f_neg_inf(), b2 = f_neg_inf();
+            double b1 = key[0], b2 = from32(kGoneHi, 0);
 #pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                b2 = fmaxf(b2, fminf(b1, v[i]));
-                b1 = fmaxf(b1, v[i]);
+            for (int i = 1; i < PL; ++i) {
+                b2 = max64(b2, min64(b1, key[i]));
+                b1 = max64(b1, key[i]);
             }
             for (int d = 1; d < a.group_lanes; d <<= 1) {
-                const float o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
-                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-                b1 = fmaxf(b1, o1);
+                const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
+                b2 = max64(min64(b1, o1), max64(b2, o2));
+                b1 = max64(b1, o1);
             }
-            const float value = pairs && b2 > f_neg_inf() ? b1 + b2 : b1;
-            int before = 0;
-            for (int h = 0; h < a.groups; ++h) {
-                const float o = __shfl(value, h * a.group_lanes, L);
-                before += o > value || (o == value && h < g);
+            const double value = pairs && !gone(b2) ? b1 + b2 : b1;
+            int before;                               // groups ahead of this lane's
+            double next;                              // the best of the groups behind it
+            auto rank_groups = [&](double v) {
+                before = 0;
+                next = from32(kGoneHi, 0);
+                for (int h = 0; h < a.groups; ++h) {
+                    const double o = __shfl(v, h * a.group_lanes, L);
+                    const bool ahead = o > v || (o == v && h < g);
+                    before += ahead;
+                    if (!ahead && h != g) next = max64(next, o);
+                }
+            };
+            rank_groups(value);
+            // the last group kept looks at the first one dropped
+            const double margin = 2.0 * tol + 2.0 * kTolChoice * fabs(value);
+            if (need_scores && before == a.kept - 1 && g < a.groups) unsure = !gone(next) && !(value - next >= margin);
+            if (__ballot(unsure) != 0) {
+                // the same by fp64 values of each group's two best; where a third expert is so near that it may be
+                // one of them, in a group near the border, the token stays unsure
+                const unsigned long long who = __ballot(unsure);
+                const double border = over_token<L>(before == a.kept - 1 && g < a.groups ? value : from32(kGoneHi, 0), MaxKey());
+                const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
+                const double c1 = gone(b1) ? b1 : choice64(t, key_expert(b1), m, total);
+                const double c2 = gone(b2) ? b2 : choice64(t, key_expert(b2), m, total);
+                const double last = pairs ? b2 : b1;
+                bool third = false;
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    third |= key[i] != b1 && key[i] != b2 && !gone(key[i]) && !(last - key[i] >= margin);
+                rank_groups(!pairs ? max64(c1, c2) : gone(b2) ? c1 : c1 + c2);
+                unsure = (who & (kToken << (lane & ~(L - 1)))) != 0 && third && !(fabs(value - border) >= 2.0 * margin);
             }
             const bool kept = before < a.kept && g < a.groups;
-            if (need_scores) {                        // fp32 scores: is the border wide enough?
-                const float lo = over_token<L>(kept ? value : -f_neg_inf(), MinOp());
-                const float hi = over_token<L>(!kept && g < a.groups ? value : f_neg_inf(), MaxOp());
-                unsure |= hi > f_neg_inf() && !(lo - hi >= 2.0f * tol + 2.0f * kTolChoice * fabsf(lo));
-            }
-#pragma unroll
-            for (int i = 0; i < PL; ++i) v[i] = !kept ? f_neg_inf() : biased ? v[i] : l[i];
-        }
-        float prev = 0.0f;
-        int slots = 0;                                // slots filled
-        for (int j = 0; j <= a.k; ++j) {
-            if (j == a.k && !biased) break;           // the pick behind the last only matters to the check
-            float best = v[0];
-#pragma unroll
-            for (int i = 1; i < PL; ++i) best = fmaxf(best, v[i]);
-            const float top = over_token<L>(best, MaxOp());
-            const bool some = top > f_neg_inf();
-            if (biased && j > 0)
-                unsure |= some && !(prev - top >= tol + kTolChoice * fabsf(prev));
-            prev = top;
-            if (j == a.k) break;
-            bool take = some && first_lane<L>(__ballot(best == top)) == q;
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
-                const bool hit = take && v[i] == top;
-                v[i] = hit ? f_neg_inf() : v[i];
-                if (hit) s_slot[wave][tok][j] = base + i;
-                take = take && !hit;
+                if (!biased && pairs) key[i] = make_key((double)l[i], base + i);   // chosen by the logit
+                key[i] = from32(kept ? hi32(key[i]) : kGoneHi, lo32(key[i]));
             }
-            slots += some;
         }
-        wave_lds_sync();
+        // picks 0 .. k-1, and with inexact keys two more: the next best, a candidate too, and the one behind it
+        double picked = from32(kGoneHi, 0), prev = 0.0;   // picked: lane j's is pick j
+        bool close = false;
+        const int rounds = biased ? a.k + 2 : a.k;
+        for (int j = 0; j < rounds; ++j) {
+            double top = key[0];
+#pragma unroll
+            for (int i = 1; i < PL; ++i) top = max64(top, key[i]);
+            top = over_token<L>(top, MaxKey());
+#pragma unroll
+            for (int i = 0; i < PL; ++i) key[i] = from32(key[i] == top ? kGoneHi : hi32(key[i]), lo32(key[i]));
+            if (biased && j > 0 && j <= a.k) close |= !gone(top) && !(prev - top >= tol + kTolChoice * fabs(prev));
+            prev = top;
+            if (q == j) picked = top;
+        }
+        bool has = q < a.k && !gone(picked);
+        int my_i = gone(picked) ? 0 : key_expert(picked);
+        if (__ballot(close) != 0) {
+            // prev is the best expert that is no candidate
+            const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
+            const bool cand = q <= a.k && !gone(picked);
+            const double c = cand ? choice64(t, my_i, m, total) : -__builtin_huge_val();
+            int rank = 0;
+            for (int j = 0; j <= a.k; ++j) {
+                const double o = __shfl(c, j, L);
+                const int oi = __shfl(my_i, j, L);
+                rank += o > c || (o == c && oi < my_i && j != q);
+            }
+            // candidates are ranked 0 .. n-1; each goes to the lane of its rank, every other lane keeps its number
+            const int to = cand ? rank : q;
+            if (close && cand && rank == a.k - 1) unsure |= !gone(prev) && !(c - prev >= tol + kTolChoice * fabs(prev));
+            const int sent = __builtin_amdgcn_ds_permute((to + (lane & ~(L - 1))) * 4, my_i);
+            my_i = close ? sent : my_i;
+        }
         // weights: lane j of the token has slot j
-        const bool has = q < slots;
-        const int my_i = has ? s_slot[wave][tok][q] : 0;
         const float x = has ? a.logits[t * a.E + my_i] : 0.0f;
         float num = 0.0f;
         if (a.renorm) {
+            // shifted by the largest factor, as in gate_row_exact
             const float f = a.sigmoid ? fminf(x, 0.0f) : x;
-            const float fm = over_token<L>(has ? f : f_neg_inf(), MaxOp());
+            const float fm = over_token<L>(has ? f : f_neg_inf(), MaxF());
             num = !has ? 0.0f : (f == fm ? 1.0f : expf(f - fm)) / (a.sigmoid ? 1.0f + expf(-fabsf(x)) : 1.0f);
-            const float tot = over_token<L>(num, AddOp());
+            const float tot = over_token<L>(num, AddF());
             num = has ? num / tot : 0.0f;
         } else if (has) {
             num = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : (x == m ? 1.0f : expf(x - m)) / sum;
         }
         const unsigned long long redo = __ballot(unsure);
-        const bool mine = ((redo >> (lane & ~(L - 1))) & 1) == 0;
+        const bool mine = (redo & (kToken << (lane & ~(L - 1)))) == 0;
         if (q < a.k && t0 + tok < a.T && mine) {
             a.idx[t * a.k + q] = has ? my_i : -1;
             a.w[t * a.k + q] = num * a.scale;
         }
         if (redo != 0) {
             for (int i = 0; i < TPW; ++i)
-                if (((redo >> (i * L)) & 1) != 0 && t0 + i < a.T) gate_row_exact<XPL>(a, t0 + i, xc);
+                if ((redo & (kToken << (i * L))) != 0 && t0 + i < a.T) gate_row_exact<XPL>(a, t0 + i, xc);
         }
-        wave_lds_sync();                              // s_slot is read before the next token's picks
     }
 }
 
@@ -441,7 +546,7 @@ bool launch_lanes(GateArgs& a, hipStream_t st) {
     int lanes = a.groups == 1 ? L : 1;
     while (lanes < L && (gs + lanes - 1) / lanes > PL) lanes *= 2;
     int per = (gs + lanes - 1) / lanes;
-    if (per > PL || lanes * a.groups > L || a.k > L) return false;
+    if (per > PL || lanes * a.groups > L || a.k >= L) return false;   // k picks and the next best, one per lane
     if (gs % 4 == 0) per = (per + 3) / 4 * 4;         // 16-byte loads
     a.group_lanes = lanes;
     a.per_lane = per;
@@ -462,8 +567,11 @@ void launch_exact(const GateArgs& a, hipStream_t st) {
 int launch_gate(GateArgs a, hipStream_t st) {
     // the lane layouts that hold the gate, the narrowest first; else (more groups than lanes) one wave per token
     // in fp64 throughout
-    if (!((a.E <= 256 && (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
-          (a.E <= 512 && launch_lanes<64, 8>(a, st)) || launch_lanes<64, 16>(a, st))) {
+    const bool few = a.T <= kFewTokens;
+    if (!((!few && a.E <= 256 &&
+           (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
+          (a.E <= 256 && launch_lanes<64, 4>(a, st)) || (a.E <= 512 && launch_lanes<64, 8>(a, st)) ||
+          launch_lanes<64, 16>(a, st))) {
         if (a.E <= 256) launch_exact<4>(a, st);
         else if (a.E <= 512) launch_exact<8>(a, st);
         else launch_exact<16>(a, st);
