@@ -17,13 +17,6 @@ namespace {
 constexpr int kMaxE = 1024;
 constexpr int kMaxK = 32;
 constexpr int kNone = 0x7fffffff;     // no expert
-#ifndef GLB
-#define GLB 2
-#endif
-#ifndef FEW
-#define FEW 2048
-#endif
-constexpr int64_t kFewTokens = FEW;
 
 struct GateArgs {
     const float* logits;              // [T,E] (split kernel: written by it, bias included)
@@ -34,8 +27,8 @@ struct GateArgs {
     float scale;
     int32_t* idx;
     float* w;
-    // lane layout of gate_lanes_kernel: a group is group_lanes lanes (a power of two) of per_lane experts
-    int group_lanes, per_lane;
+    // lane layout of gate_lanes_kernel: a group of group_size experts is 2^lane_shift lanes of per_lane experts
+    int group_size, lane_shift, per_lane;
 };
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -215,8 +208,7 @@ constexpr float kTolSoftmax = 0x1p-17f;       // >= 2 * 51 u, times 1 / S
 constexpr float kTolChoice = 0x1p-22f;        // >= 2 u, times the key
 
 constexpr uint32_t kKeyMask = 1023;           // expert numbers: E <= 1024
-constexpr uint32_t kGoneHi = 0xffefffffu;     // high word of a key that cannot be (or was) chosen: below -2^1023
-constexpr uint32_t kInfHi = 0x7e700000u;      // high word of the key of a choice of +inf: 2^1000
+constexpr uint32_t kGoneHi = 0xfe700000u;     // high word of a key that cannot be (or was) chosen: -2^1000
 
 __device__ __forceinline__ float f_neg_inf() { return -__builtin_huge_valf(); }
 __device__ __forceinline__ uint32_t hi32(double v) { return (uint32_t)(__double_as_longlong(v) >> 32); }
@@ -224,7 +216,7 @@ __device__ __forceinline__ uint32_t lo32(double v) { return (uint32_t)__double_a
 __device__ __forceinline__ double from32(uint32_t hi, uint32_t lo) {
     return __longlong_as_double((long long)(((unsigned long long)hi << 32) | lo));
 }
-__device__ __forceinline__ bool gone(double key) { return key < -0x1p1022; }
+__device__ __forceinline__ bool gone(double key) { return key < -0x1p999; }
 
 // Maximum of two numbers that are no NaN (the compiler's fmax would first quiet each operand).
 __device__ __forceinline__ double max64(double a, double b) {
@@ -239,11 +231,12 @@ __device__ __forceinline__ double min64(double a, double b) {
     return r;
 }
 
-// c as the key of expert e.  c: no NaN; -inf cannot be chosen.
-__device__ __forceinline__ double make_key(double c, int e) {
-    const uint32_t h = hi32(c), s = (uint32_t)((int32_t)h >> 31);
-    const uint32_t lo = (lo32(c) & ~kKeyMask) | ((s ^ (uint32_t)~e) & kKeyMask);
-    return from32(h == 0xfff00000u ? kGoneHi : h == 0x7ff00000u ? kInfHi : h, lo);
+// c as the key of expert e.  c: an fp32 number, no NaN (its fp64 form has the low 29 bits free); infinities
+// become +-2^1000, beyond every finite one, and -inf is an expert that cannot be chosen.
+__device__ __forceinline__ double make_key(float c, int e) {
+    const double v = min64(max64((double)c, -0x1p1000), 0x1p1000);
+    const uint32_t s = (uint32_t)((int32_t)hi32(v) >> 31);
+    return from32(hi32(v), lo32(v) | ((s ^ (uint32_t)~e) & kKeyMask));
 }
 __device__ __forceinline__ int key_expert(double key) {
     const uint32_t s = (uint32_t)((int32_t)hi32(key) >> 31);
@@ -290,14 +283,14 @@ struct MaxKey {
 };
 
 template <int L, int PL>
-__global__ __launch_bounds__(256, GLB) void gate_lanes_kernel(GateArgs a) {
+__global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     constexpr int TPW = 64 / L;                       // tokens per wave
     constexpr int XPL = L * PL <= 256 ? 4 : PL;       // experts per lane of gate_row_exact (64 lanes)
     extern __shared__ double lds[];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & (L - 1), tok = lane / L;
     double* xc = lds + wave * (a.E + a.groups);       // only laid out where groups > 1
-    const int gs = a.E / a.groups, g = q / a.group_lanes;
-    const int in_group = (q & (a.group_lanes - 1)) * a.per_lane;
+    const int gs = a.group_size, g = q >> a.lane_shift;
+    const int in_group = (q & ((1 << a.lane_shift) - 1)) * a.per_lane;
     const int base = g * gs + in_group;
     const int count = g < a.groups ? max(0, min(a.per_lane, gs - in_group)) : 0;
     const bool biased = a.balance != nullptr;
@@ -379,7 +372,7 @@ __global__ __launch_bounds__(256, GLB) void gate_lanes_kernel(GateArgs a) {
                 float c = l[i];
                 if (biased) c = b[i] > f_neg_inf() ? s[i] + b[i] : f_neg_inf();
                 else if (pairs) c = l[i] > f_neg_inf() ? s[i] : f_neg_inf();
-                key[i] = make_key((double)c, base + i);
+                key[i] = make_key(c, base + i);
             }
         }
         bool unsure = false;
@@ -390,7 +383,7 @@ __global__ __launch_bounds__(256, GLB) void gate_lanes_kernel(GateArgs a) {
                 b2 = max64(b2, min64(b1, key[i]));
                 b1 = max64(b1, key[i]);
             }
-            for (int d = 1; d < a.group_lanes; d <<= 1) {
+            for (int d = 1; d < 1 << a.lane_shift; d <<= 1) {
                 const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
                 b2 = max64(min64(b1, o1), max64(b2, o2));
                 b1 = max64(b1, o1);
@@ -402,7 +395,7 @@ __global__ __launch_bounds__(256, GLB) void gate_lanes_kernel(GateArgs a) {
                 before = 0;
                 next = from32(kGoneHi, 0);
                 for (int h = 0; h < a.groups; ++h) {
-                    const double o = __shfl(v, h * a.group_lanes, L);
+                    const double o = __shfl(v, h << a.lane_shift, L);
                     const bool ahead = o > v || (o == v && h < g);
                     before += ahead;
                     if (!ahead && h != g) next = max64(next, o);
@@ -431,7 +424,7 @@ __global__ __launch_bounds__(256, GLB) void gate_lanes_kernel(GateArgs a) {
             const bool kept = before < a.kept && g < a.groups;
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
-                if (!biased && pairs) key[i] = make_key((double)l[i], base + i);   // chosen by the logit
+                if (!biased && pairs) key[i] = make_key(l[i], base + i);   // chosen by the logit
                 key[i] = from32(kept ? hi32(key[i]) : kGoneHi, lo32(key[i]));
             }
         }
@@ -543,12 +536,14 @@ template <int L, int PL>
 bool launch_lanes(GateArgs& a, hipStream_t st) {
     // a group on the fewest lanes (a power of two) that hold it; without groups, the whole token
     const int gs = a.E / a.groups;
-    int lanes = a.groups == 1 ? L : 1;
-    while (lanes < L && (gs + lanes - 1) / lanes > PL) lanes *= 2;
-    int per = (gs + lanes - 1) / lanes;
-    if (per > PL || lanes * a.groups > L || a.k >= L) return false;   // k picks and the next best, one per lane
+    int shift = 0;
+    while ((1 << shift) < L && (a.groups == 1 || (gs + (1 << shift) - 1) >> shift > PL)) ++shift;
+    int per = (gs + (1 << shift) - 1) >> shift;
+    // k picks and the next best, one per lane
+    if (per > PL || a.groups << shift > L || a.k >= L) return false;
     if (gs % 4 == 0) per = (per + 3) / 4 * 4;         // 16-byte loads
-    a.group_lanes = lanes;
+    a.group_size = gs;
+    a.lane_shift = shift;
     a.per_lane = per;
     const int64_t waves = (a.T + 64 / L - 1) / (64 / L);
     const dim3 grid((unsigned)std::min<int64_t>((waves + 3) / 4, kMaxRowGrid));
@@ -567,7 +562,10 @@ void launch_exact(const GateArgs& a, hipStream_t st) {
 int launch_gate(GateArgs a, hipStream_t st) {
     // the lane layouts that hold the gate, the narrowest first; else (more groups than lanes) one wave per token
     // in fp64 throughout
-    const bool few = a.T <= kFewTokens;
+    // Up to 2048 tokens the chip has room for a wave each, and 64 lanes are done sooner (64 tokens x 256 experts,
+    // k = 8, sigmoid with a bias and groups: 6.5 against 8.5 us); beyond, four tokens to a wave spend fewer
+    // instructions on each (4096 tokens: 8.9 against 9.4 us; 16K: 20.5 against 33 us).
+    const bool few = a.T <= 2048;
     if (!((!few && a.E <= 256 &&
            (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
           (a.E <= 256 && launch_lanes<64, 4>(a, st)) || (a.E <= 512 && launch_lanes<64, 8>(a, st)) ||
