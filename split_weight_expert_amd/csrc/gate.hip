@@ -7,11 +7,9 @@
 #include "../../include/dwdp_layer.h"
 #include "common.h"
 #include "internal.h"
+#include "router.h"
 
 namespace dwdp {
-int router_logits(const void* x, const void* w_router, int in_dtype, const float* bias, int64_t T, int H, int E,
-                  float* logits, hipStream_t st);
-
 namespace {
 
 constexpr int kMaxE = 1024;
@@ -19,7 +17,7 @@ constexpr int kMaxK = 32;
 constexpr int kNone = 0x7fffffff;     // no expert
 
 struct GateArgs {
-    const float* logits;              // [T,E] (split kernel: written by it, bias included)
+    const float* logits;              // [T,E]
     const float* balance;             // [E] or null
     int64_t T;
     int E, k, groups, kept, group_top;
@@ -27,8 +25,14 @@ struct GateArgs {
     float scale;
     int32_t* idx;
     float* w;
+    // with a sliced router product: logits = sum of part[slices][T][E] + bias, written by gate_lanes_kernel
+    const float* part;
+    const float* bias;                // or null
+    int slices;
+    float* logits_out;
     // lane layout of gate_lanes_kernel: a group of group_size experts is 2^lane_shift lanes of per_lane experts
     int group_size, lane_shift, per_lane;
+    int64_t first;                    // its launch's first token
 };
 
 __device__ __forceinline__ void wave_lds_sync() {
@@ -282,7 +286,8 @@ struct MaxKey {
     __device__ __forceinline__ double operator()(double a, double b) const { return max64(a, b); }
 };
 
-template <int L, int PL>
+// SLICED: the logits come as a router product's partial sums, and are written on the way.
+template <int L, int PL, bool SLICED>
 __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     constexpr int TPW = 64 / L;                       // tokens per wave
     constexpr int XPL = L * PL <= 256 ? 4 : PL;       // experts per lane of gate_row_exact (64 lanes)
@@ -296,8 +301,9 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     const bool biased = a.balance != nullptr;
     const bool pairs = a.groups > 1 && a.group_top == 2;
     const bool need_scores = biased || pairs;         // keys, or groups' values, from inexact scores
-    const bool vec = (a.per_lane & 3) == 0 && (gs & 3) == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15) == 0 &&
-                     (reinterpret_cast<uintptr_t>(a.balance) & 15) == 0;
+    const bool vec = (a.per_lane & 3) == 0 && (gs & 3) == 0 &&
+                     ((reinterpret_cast<uintptr_t>(a.logits) | reinterpret_cast<uintptr_t>(a.balance) |
+                       reinterpret_cast<uintptr_t>(a.bias)) & 15) == 0;
     // PL consecutive floats of this lane, -inf behind its count (with vec, counts are multiples of 4 too)
     auto load = [&](const float* p, float* x) {
         if (vec) {
@@ -328,10 +334,48 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : (x == m ? 1.0 : exp((double)x - (double)m)) / total;
         return biased ? s + (double)a.balance[e] : s;
     };
-    for (int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * TPW; t0 < a.T; t0 += (int64_t)gridDim.x * 4 * TPW) {
+    const int64_t t0 = a.first + ((int64_t)blockIdx.x * 4 + wave) * TPW;
+    if (t0 < a.T) {
         const int64_t t = min(t0 + tok, a.T - 1);     // lanes behind the last token repeat it and write nothing
         float l[PL], b[PL];
-        load(a.logits + t * a.E + base, l);
+        if constexpr (SLICED) {
+            // slices are added in order; four are read together
+            const float* p = a.part + t * a.E + base;
+            const int64_t stride = a.T * a.E;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) l[i] = 0.0f;
+            for (int s0 = 0; s0 < a.slices; s0 += 4) {
+                float more[4][PL];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (s0 + u < a.slices) load(p + (s0 + u) * stride, more[u]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (s0 + u < a.slices)
+#pragma unroll
+                        for (int i = 0; i < PL; ++i) l[i] += more[u][i];
+            }
+            if (a.bias != nullptr) {
+                float more[PL];
+                load(a.bias + base, more);
+#pragma unroll
+                for (int i = 0; i < PL; ++i) l[i] += more[i];
+            }
+            float* out = a.logits_out + t * a.E + base;
+            if (vec) {
+#pragma unroll
+                for (int i = 0; i < PL; i += 4)
+                    if (i < count) *reinterpret_cast<float4*>(out + i) = float4{l[i], l[i + 1], l[i + 2], l[i + 3]};
+            } else {
+#pragma unroll
+                for (int i = 0; i < PL; ++i)
+                    if (i < count) out[i] = l[i];
+            }
+            // lanes of this wave read each other's logits below
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+        } else {
+            load(a.logits + t * a.E + base, l);
+        }
         if (biased) load(a.balance + base, b);
         float m = f_neg_inf();
 #pragma unroll
@@ -345,89 +389,100 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         constexpr float kLog2e = 1.44269504088896340736f;
         float sum = 1.0f;                             // the softmax's denominator in units of exp(m)
         float tol = kTolSigmoid;
-        double key[PL];
-        {
-            float s[PL];
-            if (!a.sigmoid && (need_scores || !a.renorm)) {
-                m = over_token<L>(m, MaxF());
-                sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < PL; ++i) {
-                    s[i] = l[i] == m ? 1.0f : __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
-                    s[i] = l[i] > f_neg_inf() ? s[i] : 0.0f;
-                    sum += s[i];
-                }
-                sum = over_token<L>(sum, AddF());
-                const float inv = __builtin_amdgcn_rcpf(sum);
-                tol = kTolSoftmax * inv;
-#pragma unroll
-                for (int i = 0; i < PL; ++i) s[i] *= inv;
-            } else if (need_scores) {
-#pragma unroll
-                for (int i = 0; i < PL; ++i)
-                    s[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
-            }
+        float c[PL];                                  // choices; without a bias the logits, or scores for the groups
+        if (!a.sigmoid && (need_scores || !a.renorm)) {
+            m = over_token<L>(m, MaxF());
+            sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
-                float c = l[i];
-                if (biased) c = b[i] > f_neg_inf() ? s[i] + b[i] : f_neg_inf();
-                else if (pairs) c = l[i] > f_neg_inf() ? s[i] : f_neg_inf();
-                key[i] = make_key(c, base + i);
+                c[i] = l[i] == m ? 1.0f : __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
+                c[i] = l[i] > f_neg_inf() ? c[i] : 0.0f;
+                sum += c[i];
             }
+            sum = over_token<L>(sum, AddF());
+            const float inv = __builtin_amdgcn_rcpf(sum);
+            tol = kTolSoftmax * inv;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) c[i] *= inv;
+        } else if (need_scores) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -kLog2e));
         }
-        bool unsure = false;
+        if (biased) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) c[i] = b[i] > f_neg_inf() ? c[i] + b[i] : f_neg_inf();
+        } else {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) c[i] = pairs && l[i] > f_neg_inf() ? c[i] : l[i];
+        }
+        bool unsure = false, kept = true;
         if (a.groups > 1) {
-            double b1 = key[0], b2 = from32(kGoneHi, 0);
+            float b1 = c[0], b2 = f_neg_inf();
 #pragma unroll
             for (int i = 1; i < PL; ++i) {
-                b2 = max64(b2, min64(b1, key[i]));
-                b1 = max64(b1, key[i]);
+                b2 = fmaxf(b2, fminf(b1, c[i]));
+                b1 = fmaxf(b1, c[i]);
             }
-            for (int d = 1; d < 1 << a.lane_shift; d <<= 1) {
-                const double o1 = __shfl_xor(b1, d), o2 = __shfl_xor(b2, d);
-                b2 = max64(min64(b1, o1), max64(b2, o2));
-                b1 = max64(b1, o1);
-            }
-            const double value = pairs && !gone(b2) ? b1 + b2 : b1;
-            int before;                               // groups ahead of this lane's
-            double next;                              // the best of the groups behind it
-            auto rank_groups = [&](double v) {
-                before = 0;
-                next = from32(kGoneHi, 0);
-                for (int h = 0; h < a.groups; ++h) {
-                    const double o = __shfl(v, h << a.lane_shift, L);
-                    const bool ahead = o > v || (o == v && h < g);
-                    before += ahead;
-                    if (!ahead && h != g) next = max64(next, o);
-                }
+            auto merge = [&](float o1, float o2) {
+                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+                b1 = fmaxf(b1, o1);
             };
-            rank_groups(value);
+            if (a.lane_shift > 0) merge(dpp<0xB1>(b1), dpp<0xB1>(b2));
+            if (a.lane_shift > 1) merge(dpp<0x4E>(b1), dpp<0x4E>(b2));
+            if (a.lane_shift > 2) merge(dpp<0x141>(b1), dpp<0x141>(b2));
+            if (a.lane_shift > 3) merge(dpp<0x140>(b1), dpp<0x140>(b2));
+            if (a.lane_shift > 4) merge(__shfl_xor(b1, 16), __shfl_xor(b2, 16));
+            const float value = pairs && b2 > f_neg_inf() ? b1 + b2 : b1;
+            int before = 0;                           // groups ahead of this lane's
+            float next = f_neg_inf();                 // the best of the groups behind it
+            for (int h = 0; h < a.groups; ++h) {
+                const float o = __shfl(value, h << a.lane_shift, L);
+                const bool ahead = o > value || (o == value && h < g);
+                before += ahead;
+                next = ahead || h == g ? next : fmaxf(next, o);
+            }
             // the last group kept looks at the first one dropped
-            const double margin = 2.0 * tol + 2.0 * kTolChoice * fabs(value);
-            if (need_scores && before == a.kept - 1 && g < a.groups) unsure = !gone(next) && !(value - next >= margin);
-            if (__ballot(unsure) != 0) {
+            const float margin = 2.0f * tol + 2.0f * kTolChoice * fabsf(value);
+            const bool last = before == a.kept - 1 && g < a.groups;
+            unsure = need_scores && last && next > f_neg_inf() && !(value - next >= margin);
+            const unsigned long long who = __ballot(unsure);
+            if (who != 0) {
                 // the same by fp64 values of each group's two best; where a third expert is so near that it may be
                 // one of them, in a group near the border, the token stays unsure
-                const unsigned long long who = __ballot(unsure);
-                const double border = over_token<L>(before == a.kept - 1 && g < a.groups ? value : from32(kGoneHi, 0), MaxKey());
-                const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
-                const double c1 = gone(b1) ? b1 : choice64(t, key_expert(b1), m, total);
-                const double c2 = gone(b2) ? b2 : choice64(t, key_expert(b2), m, total);
-                const double last = pairs ? b2 : b1;
+                const float border = over_token<L>(last ? value : f_neg_inf(), MaxF());
+                double k1 = make_key(c[0], base), k2 = from32(kGoneHi, 0);
+#pragma unroll
+                for (int i = 1; i < PL; ++i) {
+                    const double key = make_key(c[i], base + i);
+                    k2 = max64(k2, min64(k1, key));
+                    k1 = max64(k1, key);
+                }
+                for (int d = 1; d < 1 << a.lane_shift; d <<= 1) {
+                    const double o1 = __shfl_xor(k1, d), o2 = __shfl_xor(k2, d);
+                    k2 = max64(min64(k1, o1), max64(k2, o2));
+                    k1 = max64(k1, o1);
+                }
+                const int e1 = gone(k1) ? 0 : key_expert(k1), e2 = gone(k2) ? 0 : key_expert(k2);
                 bool third = false;
 #pragma unroll
                 for (int i = 0; i < PL; ++i)
-                    third |= key[i] != b1 && key[i] != b2 && !gone(key[i]) && !(last - key[i] >= margin);
-                rank_groups(!pairs ? max64(c1, c2) : gone(b2) ? c1 : c1 + c2);
-                unsure = (who & (kToken << (lane & ~(L - 1)))) != 0 && third && !(fabs(value - border) >= 2.0 * margin);
+                    third |= c[i] > f_neg_inf() && base + i != e1 && base + i != e2 && !((pairs ? b2 : b1) - c[i] >= margin);
+                const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
+                const double c1 = gone(k1) ? -__builtin_huge_val() : choice64(t, e1, m, total);
+                const double c2 = gone(k2) ? -__builtin_huge_val() : choice64(t, e2, m, total);
+                const double v = gone(k2) ? c1 : pairs ? c1 + c2 : fmax(c1, c2);
+                before = 0;
+                for (int h = 0; h < a.groups; ++h) {
+                    const double o = __shfl(v, h << a.lane_shift, L);
+                    before += o > v || (o == v && h < g);
+                }
+                unsure = (who & (kToken << (lane & ~(L - 1)))) != 0 && third && !(fabsf(value - border) >= 2.0f * margin);
             }
-            const bool kept = before < a.kept && g < a.groups;
-#pragma unroll
-            for (int i = 0; i < PL; ++i) {
-                if (!biased && pairs) key[i] = make_key(l[i], base + i);   // chosen by the logit
-                key[i] = from32(kept ? hi32(key[i]) : kGoneHi, lo32(key[i]));
-            }
+            kept = before < a.kept && g < a.groups;
         }
+        double key[PL];
+#pragma unroll
+        for (int i = 0; i < PL; ++i) key[i] = make_key(!kept ? f_neg_inf() : biased ? c[i] : l[i], base + i);
         // picks 0 .. k-1, and with inexact keys two more: the next best, a candidate too, and the one behind it
         double picked = from32(kGoneHi, 0), prev = 0.0;   // picked: lane j's is pick j
         bool close = false;
@@ -545,10 +600,15 @@ bool launch_lanes(GateArgs& a, hipStream_t st) {
     a.group_size = gs;
     a.lane_shift = shift;
     a.per_lane = per;
-    const int64_t waves = (a.T + 64 / L - 1) / (64 / L);
-    const dim3 grid((unsigned)std::min<int64_t>((waves + 3) / 4, kMaxRowGrid));
     const size_t lds = a.groups > 1 ? 4 * (size_t)(a.E + a.groups) * sizeof(double) : 0;   // for gate_row_exact
-    hipLaunchKernelGGL((gate_lanes_kernel<L, PL>), grid, dim3(256), lds, st, a);
+    constexpr int64_t kTokens = 4 * (64 / L);         // per workgroup
+    // a launch takes up to kMaxRowGrid workgroups (a loop over tokens in the kernel would keep what is the same
+    // for all of them in registers: 200 instead of 131)
+    for (a.first = 0; a.first < a.T; a.first += kMaxRowGrid * kTokens) {
+        const dim3 grid((unsigned)std::min<int64_t>((a.T - a.first + kTokens - 1) / kTokens, kMaxRowGrid));
+        if (a.part != nullptr) hipLaunchKernelGGL((gate_lanes_kernel<L, PL, true>), grid, dim3(256), lds, st, a);
+        else hipLaunchKernelGGL((gate_lanes_kernel<L, PL, false>), grid, dim3(256), lds, st, a);
+    }
     return true;
 }
 
@@ -559,20 +619,29 @@ void launch_exact(const GateArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(gate_exact_kernel<PL>, grid, dim3(256), lds, st, a);
 }
 
+// Whether a lane layout holds the gate: a group on at most 64 / groups lanes, a power of two.
+bool lanes_hold(const GateArgs& a) {
+    if (a.groups > 64) return false;
+    int lanes = 1;
+    while (2 * lanes * a.groups <= 64) lanes *= 2;
+    return (a.E / a.groups + lanes - 1) / lanes <= 16;
+}
+
 int launch_gate(GateArgs a, hipStream_t st) {
-    // the lane layouts that hold the gate, the narrowest first; else (more groups than lanes) one wave per token
-    // in fp64 throughout
     // Up to 2048 tokens the chip has room for a wave each, and 64 lanes are done sooner (64 tokens x 256 experts,
     // k = 8, sigmoid with a bias and groups: 6.5 against 8.5 us); beyond, four tokens to a wave spend fewer
     // instructions on each (4096 tokens: 8.9 against 9.4 us; 16K: 20.5 against 33 us).
     const bool few = a.T <= 2048;
-    if (!((!few && a.E <= 256 &&
-           (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
-          (a.E <= 256 && launch_lanes<64, 4>(a, st)) || (a.E <= 512 && launch_lanes<64, 8>(a, st)) ||
-          launch_lanes<64, 16>(a, st))) {
-        if (a.E <= 256) launch_exact<4>(a, st);
-        else if (a.E <= 512) launch_exact<8>(a, st);
-        else launch_exact<16>(a, st);
+    if (lanes_hold(a)) {
+        // the narrowest layout that holds it
+        (!few && (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
+            launch_lanes<64, 4>(a, st) || launch_lanes<64, 8>(a, st) || launch_lanes<64, 16>(a, st);
+    } else if (a.E <= 256) {
+        launch_exact<4>(a, st);
+    } else if (a.E <= 512) {
+        launch_exact<8>(a, st);
+    } else {
+        launch_exact<16>(a, st);
     }
     DWDP_LAUNCHED();
     return DWDP_OK;
@@ -596,8 +665,11 @@ extern "C" int dwdp_gate_topk(const float* logits, const float* balance_bias, in
 }
 
 extern "C" size_t dwdp_route_gate_workspace_bytes(int64_t T, int H, int E, int in_dtype) {
-    (void)T, (void)H, (void)E, (void)in_dtype;
-    return 0;
+    if (T < 1 || T >= ((int64_t)1 << 31) || E < 1 || E > kMaxE || (in_dtype != DWDP_F32 && in_dtype != DWDP_BF16) ||
+        H < 1 || H % (in_dtype == DWDP_BF16 ? 64 : 16) != 0)
+        return 0;
+    const RouterPlan p = plan_router(T, H, E, in_dtype);
+    return p.slices == 1 ? 0 : (size_t)p.slices * T * E * sizeof(float);
 }
 
 extern "C" int dwdp_route_gate(const void* x, const void* w_router, int in_dtype, const float* bias,
@@ -622,7 +694,17 @@ extern "C" int dwdp_route_gate(const void* x, const void* w_router, int in_dtype
         if (ws_bytes < need) return fail(DWDP_ERR_WORKSPACE, "dwdp_route_gate: workspace too small");
     }
     hipStream_t st = as_stream(stream);
-    rc = router_logits(x, w_router, in_dtype, bias, T, H, E, logits_out, st);
+    GateArgs a = gate_args(logits_out, balance_bias, T, E, *gate, topk_idx, topk_w);
+    const RouterPlan p = plan_router(T, H, E, in_dtype);
+    if (p.slices > 1 && lanes_hold(a)) {
+        a.part = static_cast<const float*>(ws);
+        a.bias = bias;
+        a.slices = p.slices;
+        a.logits_out = logits_out;
+        rc = router_split(x, w_router, in_dtype, bias, T, H, E, p, logits_out, static_cast<float*>(ws), st);
+    } else {
+        rc = router_split(x, w_router, in_dtype, bias, T, H, E, RouterPlan{p.bm, p.bn, 1}, logits_out, nullptr, st);
+    }
     if (rc != DWDP_OK) return rc;
-    return launch_gate(gate_args(logits_out, balance_bias, T, E, *gate, topk_idx, topk_w), st);
+    return launch_gate(a, st);
 }

@@ -1,0 +1,283 @@
+// The router product of dwdp_route_gate: logits = x w^T with the columns of K cut into slices, so that
+// every batch fills the chip.  With one slice the logits are written (bias added); with more, each slice's
+// partial sums go to part[slice][T][E] and the gate's kernel adds them, in slice order, as it reads them.
+//
+//   few tokens   router_few_kernel: 16 x 16 tiles, operands straight from global memory into the matrix
+//                instruction; bound by latency, and by the weights' bytes
+//   many tokens  router_tile_kernel: BM x BN tiles, operands by DMA into an LDS ring; bound by the tokens'
+//                bytes and the matrix cores
+#include <algorithm>
+
+#include "common.h"
+#include "internal.h"
+#include "router.h"
+
+namespace dwdp {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct RouterArgs {
+    const uint8_t* x;
+    const uint8_t* w;
+    const float* bias;                // or null
+    int64_t T;
+    int H, E, slices, m_tiles, n_tiles;
+    float* out;                       // logits (one slice) or part
+};
+
+__device__ __forceinline__ void store_logit(const RouterArgs& a, int slice, int64_t t, int e, float v) {
+    if (t >= a.T || e >= a.E) return;
+    if (a.slices == 1) a.out[t * a.E + e] = v + (a.bias ? a.bias[e] : 0.0f);
+    else a.out[(slice * a.T + t) * a.E + e] = v;
+}
+
+// One 16-token x 16-expert tile of one slice; the slice's K steps are split over the workgroup's waves and
+// their partial tiles summed through LDS in wave order.  Operand lanes: row (or expert) l % 16 and 16 bytes at
+// 16 (l / 16) of the step; a step is 64 bytes of a row.  bf16: one v_mfma_f32_16x16x32_bf16 a step; fp32: four
+// v_mfma_f32_16x16x4_f32, each taking one of the four consecutive columns a lane holds, which is the same
+// columns on both sides.  Result element r of lane l: token 4 (l / 16) + r, expert l % 16.
+constexpr int kFewWaves = 4;
+
+template <bool BF16>
+__global__ __launch_bounds__(kFewWaves * 64) void router_few_kernel(RouterArgs a) {
+    __shared__ float part[kFewWaves][64][5];      // 5: consecutive lanes fall on different banks
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, q = lane >> 4;
+    const int n = blockIdx.x % a.n_tiles, ms = blockIdx.x / a.n_tiles, slice = ms % a.slices;
+    const int64_t m0 = (int64_t)(ms / a.slices) * 16;
+    const int n0 = n * 16;
+    const int64_t row_bytes = (int64_t)a.H * (BF16 ? 2 : 4);
+    const uint8_t* xr = a.x + min(m0 + l16, a.T - 1) * row_bytes + q * 16;
+    const uint8_t* wr = a.w + (int64_t)min(n0 + l16, a.E - 1) * row_bytes + q * 16;
+    const int steps = (int)(row_bytes / 64);
+    const int s0 = (int)((int64_t)slice * steps / a.slices), ns = (int)((int64_t)(slice + 1) * steps / a.slices) - s0;
+    const int sb = s0 + wave * ns / kFewWaves, se = s0 + (wave + 1) * ns / kFewWaves;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int U = 8;                          // steps whose loads are in flight together
+    for (int s = sb; s < se; s += U) {
+        f32x4 xa[U], wa[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s + u < se) {
+                xa[u] = *reinterpret_cast<const f32x4*>(xr + (int64_t)(s + u) * 64);
+                wa[u] = *reinterpret_cast<const f32x4*>(wr + (int64_t)(s + u) * 64);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s + u < se) {
+                if constexpr (BF16) {
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xa[u]),
+                                                                  __builtin_bit_cast(bf16x8, wa[u]), acc, 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(xa[u][c], wa[u][c], acc, 0, 0, 0);
+                }
+            }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) part[wave][lane][r] = acc[r];
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float s = part[0][lane][r];
+#pragma unroll
+            for (int w = 1; w < kFewWaves; ++w) s += part[w][lane][r];
+            store_logit(a, slice, m0 + q * 4 + r, n0 + l16, s);
+        }
+    }
+}
+
+// 16 bytes per lane from global memory to LDS, lane l at byte 16 l of `lds` (wave-uniform).
+__device__ __forceinline__ void dma16(const uint8_t* g, uint8_t* lds) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
+                                     (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    static_assert(N >= 0 && N < 64, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+}
+
+__device__ __forceinline__ void ordered_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+template <int PER, int MOST>
+__device__ __forceinline__ void wait_steps(int steps) {   // at most `steps` (<= MOST) batches of PER loads outstanding
+    if constexpr (MOST == 0) wait_vmcnt<0>();
+    else if (steps >= MOST) wait_vmcnt<PER * MOST>();
+    else wait_steps<PER, MOST - 1>(steps);
+}
+
+// One BM x BN tile of one slice, bf16.  WM x WN waves; a K step is 64 columns, 128 bytes of a row, moved into LDS
+// by 1 KB DMA instructions of 8 rows each, into a ring of NS slots with NS - 1 steps in flight.  The slot of step
+// k + NS - 1 is the one step k - 1 read, so it is filled after step k's barrier, and its DMAs are issued between
+// the step's products: issued in one go they hold up the wave, and with it the products, for as long as the
+// address unit takes them.  16-byte chunk c of row r sits in slot c ^ ((r / 2) % 8) of its row, so that 16
+// consecutive rows read at one chunk spread over all banks.
+template <int BM, int BN, int WM, int WN, int NS>
+__global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a) {
+    constexpr int NW = WM * WN, ROWB = 128, STAGE = (BM + BN) * ROWB, P = NS - 1;
+    constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NJ = TN / 32;
+    constexpr int PER = (BM + BN) / 8 / NW;       // DMA instructions per wave and step
+    static_assert((BM + BN) / 8 % NW == 0 && PER * P < 64, "rows split evenly over the waves");
+    static_assert(NS * STAGE <= 163840, "LDS");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[NS * STAGE];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN, l32 = lane & 31, hi = lane >> 5;
+    // Workgroup b runs on XCD b % 8.  Each XCD takes a run of consecutive tiles, token tiles innermost, so that
+    // the weights it multiplies by (one slice, nearly always) stay in its L2.
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles * a.slices, per_xcd = (tiles + kNumXcd - 1) / kNumXcd;
+    const int64_t lin = blockIdx.x % kNumXcd * per_xcd + blockIdx.x / kNumXcd;
+    if (blockIdx.x / kNumXcd >= per_xcd || lin >= tiles) return;
+    const int m = (int)(lin % a.m_tiles), n = (int)(lin / a.m_tiles % a.n_tiles), slice = (int)(lin / a.m_tiles / a.n_tiles);
+    const int64_t m0 = (int64_t)m * BM;
+    const int n0 = n * BN;
+    const int steps = a.H / 64;
+    const int kb = (int)((int64_t)slice * steps / a.slices), KT = (int)((int64_t)(slice + 1) * steps / a.slices) - kb;
+
+    const uint8_t* g[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int r = (wave * PER + i) * 8 + lane / 8;    // row of the stage: BM token rows, then BN expert rows
+        const int c = (lane & 7) ^ ((r >> 1) & 7);
+        g[i] = (r < BM ? a.x + min(m0 + r, a.T - 1) * a.H * 2 : a.w + (int64_t)min(n0 + r - BM, a.E - 1) * a.H * 2) +
+               (int64_t)kb * ROWB + c * 16;
+    }
+    auto issue = [&](int kt, int i) {
+        dma16(g[i] + (int64_t)kt * ROWB, ring + kt % NS * STAGE + (wave * PER + i) * 1024);
+    };
+    auto frag = [&](const uint8_t* s, int row, int chunk) {
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const f32x4*>(s + row * ROWB + ((chunk ^ ((row >> 1) & 7)) << 4)));
+    };
+    f32x16 acc[MI][NJ];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    for (int k = 0; k < P && k < KT; ++k)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) issue(k, i);
+    for (int kt = 0; kt < KT; ++kt) {
+        // this wave's DMAs of step kt have landed once at most those of the later issued steps are out
+        wait_steps<PER, P - 1>(min(P - 1, KT - 1 - kt));
+        ordered_barrier();                        // every wave's step kt landed; step kt-1's slot is free
+        const uint8_t* A = ring + kt % NS * STAGE;
+        const uint8_t* B = A + BM * ROWB;
+        const bool more = kt + P < KT;
+        bf16x8 af[4][MI], bf[4][NJ];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) af[s][i] = frag(A, wm * TM + i * 32 + l32, 2 * s + hi);
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) bf[s][j] = frag(B, wn * TN + j * 32 + l32, 2 * s + hi);
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[s][i], bf[s][j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if (more)
+#pragma unroll
+                for (int i = PER * s / 4; i < PER * (s + 1) / 4; ++i) issue(kt + P, i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // the fragments are in registers before any wave passes the next barrier
+        __builtin_amdgcn_s_waitcnt(0xC07F);       // lgkmcnt(0); vmcnt and expcnt not waited on
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                store_logit(a, slice, m0 + wm * TM + i * 32 + (r >> 2) * 8 + hi * 4 + (r & 3), n0 + wn * TN + j * 32 + l32,
+                            acc[i][j][r]);
+}
+
+template <int BM, int BN, int WM, int WN, int NS>
+void launch_tile(const RouterArgs& a, hipStream_t st) {
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles * a.slices;
+    const unsigned grid = (unsigned)((tiles + kNumXcd - 1) / kNumXcd * kNumXcd);
+    hipLaunchKernelGGL((router_tile_kernel<BM, BN, WM, WN, NS>), dim3(grid), dim3(WM * WN * 64), 0, st, a);
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+// Measured on 7168-wide bf16 tokens and 256 experts, product and gate together, other inputs in between:
+//   tokens     64: 16 x 16 tiles 14.2 us, 64 x 64 tiles 15.2          128: 16.7 and 15.5
+//   tokens   1024: 64 x 64 tiles 19.2 us, 64 x 256 21.7              2048: 25.4 and 25.8    4096: 45.6 and 36.6
+//   tokens   4096: 64 x 256 tiles 36.6 us, 128 x 256 40.1            8192: 64.5 and 58.5
+// Slices: as many as give the chip's 256 compute units a tile each (two of the 64 x 64 ones), but no more than 8,
+// since the gate reads what every slice writes (one token: 8 slices 10.7 us, 16 12.4), of 4 K steps at least.
+RouterPlan plan_router(int64_t T, int H, int E, int dtype) {
+    RouterPlan p{};
+    const int64_t t64 = ceil_div(T, 64);
+    int64_t want = 256;
+    if (dtype != DWDP_BF16 || T <= 64) {
+        p.bm = p.bn = 16;
+    } else if (E <= 64 || t64 * ceil_div(E, 64) <= 128) {
+        p.bm = p.bn = 64;
+        want = 512;
+    } else if (E <= 128) {
+        p.bm = 64;
+        p.bn = 128;
+    } else {
+        p.bm = t64 * ceil_div(E, 256) >= 128 ? 128 : 64;
+        p.bn = 256;
+    }
+    const int64_t tiles = ceil_div(T, p.bm) * ceil_div(E, p.bn);
+    const int64_t steps = (int64_t)H * (dtype == DWDP_BF16 ? 2 : 4) / (p.bm == 16 ? 64 : 128);
+    p.slices = (int)std::max<int64_t>(1, std::min({want / tiles, steps / 4, (int64_t)8}));
+    return p;
+}
+
+int router_split(const void* x, const void* w, int dtype, const float* bias, int64_t T, int H, int E, const RouterPlan& p,
+                 float* logits, float* part, hipStream_t st) {
+    RouterArgs a{};
+    a.x = static_cast<const uint8_t*>(x);
+    a.w = static_cast<const uint8_t*>(w);
+    a.bias = bias;
+    a.T = T;
+    a.H = H;
+    a.E = E;
+    a.slices = p.slices;
+    a.m_tiles = (int)ceil_div(T, p.bm);
+    a.n_tiles = (int)ceil_div(E, p.bn);
+    a.out = p.slices == 1 ? logits : part;
+    const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles * a.slices;
+    DWDP_REQUIRE((tiles + kNumXcd) * 512 <= kMaxLaunchItems, "T too large for one router launch");
+    if (p.bm == 16) {
+        const dim3 grid((unsigned)tiles), block(kFewWaves * 64);
+        if (dtype == DWDP_BF16) hipLaunchKernelGGL(router_few_kernel<true>, grid, block, 0, st, a);
+        else hipLaunchKernelGGL(router_few_kernel<false>, grid, block, 0, st, a);
+    } else if (p.bm == 128) {
+        launch_tile<128, 256, 2, 4, 3>(a, st);
+    } else if (p.bn == 256) {
+        launch_tile<64, 256, 2, 4, 4>(a, st);
+    } else if (p.bn == 128) {
+        launch_tile<64, 128, 2, 2, 3>(a, st);
+    } else {
+        launch_tile<64, 64, 2, 2, 4>(a, st);
+    }
+    DWDP_LAUNCHED();
+    return DWDP_OK;
+}
+
+}  // namespace dwdp
