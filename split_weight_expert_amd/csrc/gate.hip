@@ -256,11 +256,26 @@ __device__ __forceinline__ double dpp(double v) {
     return from32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi32(v), CTRL, 0xf, 0xf, true),
                   (uint32_t)__builtin_amdgcn_update_dpp(0, (int)lo32(v), CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float read_lane(float v, int l) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+// This lane's and its partner's number (16 or 32 lanes away), in the order of the lanes.
+template <int D>
+__device__ __forceinline__ void swap_pair(uint32_t v, uint32_t& a, uint32_t& b) {
+    const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0];
+    b = r[1];
 }
-__device__ __forceinline__ double read_lane(double v, int l) {
-    return from32((uint32_t)__builtin_amdgcn_readlane((int)hi32(v), l), (uint32_t)__builtin_amdgcn_readlane((int)lo32(v), l));
+template <int D, class Op>
+__device__ __forceinline__ float with_partner(float v, Op op) {
+    uint32_t a, b;
+    swap_pair<D>(__float_as_uint(v), a, b);
+    return op(__uint_as_float(a), __uint_as_float(b));
+}
+template <int D, class Op>
+__device__ __forceinline__ double with_partner(double v, Op op) {
+    uint32_t ah, bh, al, bl;
+    swap_pair<D>(hi32(v), ah, bh);
+    swap_pair<D>(lo32(v), al, bl);
+    return op(from32(ah, al), from32(bh, bl));
 }
 
 // Over the L lanes of a token, the same in each of them.
@@ -270,7 +285,7 @@ __device__ __forceinline__ V over_token(V v, Op op) {
     v = op(v, dpp<0x4E>(v));                  // 2 apart
     v = op(v, dpp<0x141>(v));                 // mirrored in 8
     v = op(v, dpp<0x140>(v));                 // mirrored in 16
-    if constexpr (L == 64) v = op(op(read_lane(v, 0), read_lane(v, 16)), op(read_lane(v, 32), read_lane(v, 48)));
+    if constexpr (L == 64) v = with_partner<32>(with_partner<16>(v, op), op);
     return v;
 }
 struct MaxF {
@@ -431,7 +446,9 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
             if (a.lane_shift > 1) merge(dpp<0x4E>(b1), dpp<0x4E>(b2));
             if (a.lane_shift > 2) merge(dpp<0x141>(b1), dpp<0x141>(b2));
             if (a.lane_shift > 3) merge(dpp<0x140>(b1), dpp<0x140>(b2));
-            if (a.lane_shift > 4) merge(__shfl_xor(b1, 16), __shfl_xor(b2, 16));
+            if constexpr (L == 64) {
+                if (a.lane_shift > 4) merge(__shfl_xor(b1, 16), __shfl_xor(b2, 16));
+            }
             const float value = pairs && b2 > f_neg_inf() ? b1 + b2 : b1;
             int before = 0;                           // groups ahead of this lane's
             float next = f_neg_inf();                 // the best of the groups behind it
