@@ -239,7 +239,11 @@ def _gpu_index(name, t):
 
 
 def _raw_stream(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device_index != index:
+        raise ValueError(f"the stream belongs to GPU {stream.device_index}, the tensors are on GPU {index}")
+    return stream.cuda_stream
 
 
 def _matrix(name, t):

@@ -646,8 +646,8 @@ bool lanes_hold(const GateArgs& a) {
 
 int launch_gate(GateArgs a, hipStream_t st) {
     // Up to 2048 tokens the chip has room for a wave each, and 64 lanes are done sooner (64 tokens x 256 experts,
-    // k = 8, sigmoid with a bias and groups: 6.5 against 8.5 us); beyond, four tokens to a wave spend fewer
-    // instructions on each (4096 tokens: 8.9 against 9.4 us; 16K: 20.5 against 33 us).
+    // k = 8, sigmoid with a bias and groups: 5.3 against 6.8 us); beyond, four tokens to a wave spend fewer
+    // instructions on each (4096 tokens: 7.1 against 7.9 us; 16K: 13.8 against 22.6).
     const bool few = a.T <= 2048;
     if (lanes_hold(a)) {
         // the narrowest layout that holds it

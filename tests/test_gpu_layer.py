@@ -585,3 +585,149 @@ def test_side_stream_and_graph_replays():
         for n in og:
             assert torch.equal(og[n].view(torch.uint8), oe[n].view(torch.uint8)), (i, n)
             assert torch.equal(os_[n].view(torch.uint8), oe[n].view(torch.uint8)), (i, n)
+
+
+# ------------------------------------------------------------------------------------------------ every lane layout
+
+def special_rows(E, g):
+    """Rows where the choice can go wrong: equal and nearly equal logits, masked and non-finite ones."""
+    inf, nan = float("inf"), float("nan")
+    l = torch.randn(64, E, generator=g, device=DEV)
+    l[0] = 0.75
+    l[1:5] = torch.randint(0, 3, (4, E), generator=g, device=DEV).float() * 0.5
+    l[5:13] = 1.0 + torch.randint(0, 3, (8, E), generator=g, device=DEV).float() * 2.0 ** -23
+    l[13] = torch.where(torch.rand(E, generator=g, device=DEV) < 0.5, 0.0, -0.0)
+    l[14] = -inf
+    l[15] = nan
+    l[16] = -inf
+    l[16, E - 1] = 0.5
+    l[17, : E // 2] = nan
+    l[18, E // 3] = inf
+    l[19, [0, E - 1]] = inf
+    l[20] = torch.finfo(torch.float32).min
+    l[21, 1:] = torch.finfo(torch.float32).min
+    l[22, ::2] = -inf
+    l[23:27] = torch.where(torch.rand(4, E, generator=g, device=DEV) < 0.8, -inf, l[23:27])
+    l[27] *= 1e30
+    l[28] -= 2000.0
+    return l
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,top,k", [
+    (256, 1, 1, 1, 8), (256, 8, 4, 2, 8), (256, 8, 4, 1, 15), (256, 2, 1, 2, 8), (256, 16, 3, 2, 8), (200, 1, 1, 1, 20), (128, 8, 2, 2, 6),
+    (120, 8, 3, 2, 6), (64, 4, 2, 1, 4), (60, 12, 5, 2, 6), (30, 2, 1, 2, 5), (7, 1, 1, 1, 3), (254, 2, 1, 1, 9), (512, 8, 4, 2, 8), (300, 5, 2, 2, 7),
+    (1024, 16, 4, 2, 8), (1000, 1, 1, 1, 12), (96, 96, 10, 2, 8)])
+def test_few_and_many_tokens_choose_alike(E, groups, kept, top, k, score):
+    """The same rows alone and among thousands (other lane layouts): the same experts, the fp64 ones."""
+    g = gen(E * 100 + groups * 10 + k)
+    l = special_rows(E, g)
+    many = l.repeat(36, 1)                              # 2304 rows
+    biases = [None, torch.randn(E, generator=g, device=DEV) * 0.05, torch.randint(0, 3, (E,), generator=g, device=DEV).float() * 2.0 ** -22]
+    biases[1][E // 2] = -float("inf")
+    for balance in biases:
+        for renorm in (True, False):
+            gate = make_gate(k, score, groups, kept, top, renorm, 1.5)
+            i1, w1 = run_gate(l, gate, balance)
+            check_gate(l, gate, balance, i1, w1)
+            i2, w2 = run_gate(many, gate, balance)
+            assert torch.equal(i2.view(36, 64, k), i1.expand(36, 64, k))
+            assert torch.equal(w2.view(36, 64, k), w2[:64].expand(36, 64, k))
+            check_gate(l, gate, balance, i2[:64], w2[:64])
+
+
+def torch_gate(l, gate, balance):
+    """The gate's choice in fp64 by torch (finite logits)."""
+    x = l.double()
+    s = torch.sigmoid(x) if gate.score == "sigmoid" else torch.softmax(x, 1)
+    c = s if balance is None else s + balance.double()
+    if gate.topk_groups < gate.n_groups:
+        by = c.view(len(c), gate.n_groups, -1)
+        val = by.topk(min(gate.group_top, by.shape[2]), 2).values.sum(2)
+        keep = torch.zeros_like(val, dtype=torch.bool)
+        keep.scatter_(1, val.sort(dim=1, descending=True, stable=True).indices[:, :gate.topk_groups], True)
+        c = torch.where(keep[:, :, None], by, -float("inf")).view_as(c)
+    idx = c.sort(dim=1, descending=True, stable=True).indices[:, :gate.k]
+    w = s.gather(1, idx)
+    return idx.to(torch.int32), (w / w.sum(1, keepdim=True) if gate.renormalize else w) * gate.scale
+
+
+@pytest.mark.parametrize("E,groups,kept,top,k,score,T", [
+    (256, 8, 4, 2, 8, "sigmoid", 60000), (256, 8, 4, 1, 8, "sigmoid", 60000), (256, 1, 1, 1, 8, "sigmoid", 60000),
+    (256, 1, 1, 1, 8, "softmax", 60000), (256, 8, 3, 2, 6, "softmax", 60000), (160, 8, 3, 2, 6, "sigmoid", 30000),
+    (60, 1, 1, 1, 6, "sigmoid", 60000), (256, 8, 4, 2, 8, "sigmoid", 2000), (512, 8, 4, 2, 8, "sigmoid", 20000),
+    (1024, 16, 4, 2, 8, "sigmoid", 10000), (1000, 1, 1, 1, 12, "softmax", 10000)])
+def test_close_calls_of_many_tokens(E, groups, kept, top, k, score, T):
+    """Enough ordinary tokens that some hundreds have choices, or groups, that fp32 cannot tell apart."""
+    g = gen(E + T)
+    l = torch.randn(T, E, generator=g, device=DEV) * 1.5
+    balance = torch.randn(E, generator=g, device=DEV) * 0.05
+    for bal in (balance, None):
+        gate = make_gate(k, score, groups, kept, top, True, 2.5)
+        idx, w = run_gate(l, gate, bal)
+        oi, ow = torch_gate(l, gate, bal)
+        assert torch.equal(idx, oi), int((idx != oi).any(1).sum())
+        np.testing.assert_array_less((w.double() - ow).abs().cpu().numpy(),
+                                     weight_tolerance(l.cpu().numpy(), oi.cpu().numpy(), ow.cpu().numpy()) + 1e-38)
+
+
+# ------------------------------------------------------------------------------------------------ far offsets
+
+def test_gate_of_more_tokens_than_one_launch_takes():
+    """17M tokens: more than 2^20 workgroups of 16 tokens."""
+    T = 17_000_000
+    l = torch.randn(T, 4, generator=gen(1), device=DEV)
+    idx, w = run_gate(l, make_gate(1, "sigmoid", renorm=False))
+    assert torch.equal(idx[:, 0].long(), l.argmax(1))
+    assert (w[:, 0].double() - torch.sigmoid(l.double().amax(1))).abs().max() < 1e-6
+
+
+def test_elements_past_32_bits():
+    """Arrays of more than 2^31 elements: the last rows are right."""
+    from split_weight_expert_amd import api
+    T, H, n = 310_000, 7168, 40                       # 2.2e9 elements
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device=DEV)
+    xs, rs, w = norm_case(n, H, "bf16", 3)
+    x[-n:] = xs
+    y = torch.empty_like(x)
+    q = torch.empty(T, H, dtype=torch.uint8, device=DEV)
+    qs = torch.empty(T, H // 128, device=DEV)
+    api.add_rmsnorm(x, None, w, 1e-6, None, y, q, qs)
+    torch.cuda.synchronize()
+    z = xs.double().cpu().numpy()
+    check_norm(z, 0 * z, w.double().cpu().numpy(), 1e-6, "bf16", None, y[-n:], q[-n:], qs[-n:])
+    assert (y[:1000] == 0).all()
+    # y as the permuted rows of 34444 tokens of 8 + 1 rows each, the last of which read the last rows
+    k, Tc = 8, 34_444
+    inv = torch.arange(Tc * k, device=DEV, dtype=torch.int32).view(Tc, k)
+    wt = torch.softmax(torch.randn(Tc, k, generator=gen(4), device=DEV), 1)
+    yp = y[: Tc * (k + 1)]
+    yp[-3:] = xs[:3]
+    yp[Tc * k - 3 * k: Tc * k] = xs[: 3 * k]
+    out = torch.empty(Tc, H, dtype=torch.bfloat16, device=DEV)
+    api.combine_add_rmsnorm(yp, inv, wt, 1, None, None, 0.0, sum_out=out)
+    small = torch.cat([xs[: 3 * k], xs[:3]])
+    o1 = torch.empty(3, H, dtype=torch.bfloat16, device=DEV)
+    api.combine_add_rmsnorm(small, torch.arange(3 * k, device=DEV, dtype=torch.int32).view(3, k), wt[-3:].contiguous(), 1, None,
+                            None, 0.0, sum_out=o1)
+    assert torch.equal(out[-3:], o1)
+    # and as tokens of the router
+    xg, wr, _ = route_inputs(n, H, 256, "bf16", 5)
+    x[-n:] = xg
+    gate = make_gate(8, "sigmoid", 8, 4, 2)
+    idx, tw, lo = gate_outputs(T, 8, 256)
+    api.route_gate(x, wr, gate, lo[:T], idx[:T], tw[:T], route_ws(T, H, 256, x)[1])
+    torch.cuda.synchronize()
+    assert torch.equal(lo[T - n:T].cpu().double(), xg.double().cpu() @ wr.double().cpu().t())
+    check_gate(lo[T - n:T], gate, None, idx[T - n:T], tw[T - n:T])
+    assert (lo[:1000] == 0).all() and (idx[:1000] == torch.arange(8, device=DEV)).all()
+
+
+def test_a_stream_and_its_tensors():
+    from split_weight_expert_amd import api
+    x = torch.zeros(4, 256, device=DEV)
+
+    class Other:
+        device_index, cuda_stream = 7, 0
+    with pytest.raises(ValueError, match="belongs to GPU 7"):
+        api.add_rmsnorm(x, None, x[0], 1e-6, y=torch.empty_like(x), stream=Other())
