@@ -84,7 +84,8 @@ int dwdp_gate_topk(const float* logits, const float* balance_bias, int64_t T, in
  *   n = z / sqrt(mean(z^2) + eps) * weight, in fp32 from the unrounded z
  *   y = n rounded to dtype                                         (NULL: not written)
  *   q, q_scale = n quantised like dwdp_quantize_tokens_fp8 quantises a row, from the unrounded n: per
- *   128 columns scale = amax/448 (1 when amax is 0), code = E4M3(n/scale)   (NULL, both: not written)
+ *   128 columns scale = amax/448 (1 when amax is 0, 2^-126 where amax/448 is less), code = E4M3(n/scale)
+   (NULL, both: not written)
  * At least one of y and q is given.  Non-finite values follow IEEE arithmetic; a NaN in a 128-column
  * group makes its scale and its codes NaN.  z^2 is summed in fp32: rows whose sum of squares passes
  * 3.4e38 norm to zero.

@@ -4,6 +4,7 @@
 // fp32 until the one rounding of each output.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/dwdp_layer.h"
 #include "common.h"
@@ -14,9 +15,6 @@ namespace {
 
 constexpr int kMaxK = 64;
 constexpr int kFewRows = 512;
-constexpr int kManyC = 2;
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct NormArgs {
     // z's source
@@ -37,113 +35,159 @@ struct NormArgs {
     float* q_scale;
 };
 
-// VEC consecutive elements (8: 16-byte accesses; 1: element accesses) of a bf16 or fp32 array.
-template <bool BF16, int VEC>
-__device__ __forceinline__ void load_vec(const uint8_t* p, int64_t i, float* v) {
-    if constexpr (VEC == 1) {
-        v[0] = BF16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
-    } else if constexpr (BF16) {
-        const uint4 r = *reinterpret_cast<const uint4*>(p + i * 2);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-    } else {
-        const float4 a = *reinterpret_cast<const float4*>(p + i * 4);
-        const float4 b = *reinterpret_cast<const float4*>(p + i * 4 + 16);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
 
-// 16 bytes that this launch reads once.
-__device__ __forceinline__ float4 load_stream(const uint8_t* p) {
-    const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p));
-    return float4{v[0], v[1], v[2], v[3]};
+// Sum over LANES (16, 32 or 64) lanes, the same in each of them: exchanges inside rows of 16 lanes, then swaps of
+// rows and of halves.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
+    auto add = [&](uint32_t o) { v += __uint_as_float(o); };
+    add(dpp<0xB1>(__float_as_uint(v)));        // lanes 1 apart
+    add(dpp<0x4E>(__float_as_uint(v)));        // 2 apart
+    add(dpp<0x141>(__float_as_uint(v)));       // mirrored in 8
+    add(dpp<0x140>(__float_as_uint(v)));       // mirrored in 16
+    if constexpr (LANES >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    if constexpr (LANES == 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return v;
+}
+
+// Eight consecutive elements are read and written together.  EVEN: rows of a multiple of 8 elements at 16-byte
+// aligned addresses; else addresses are aligned to the element only, which the hardware's 16-byte accesses allow,
+// and the last vector of a row has fewer valid elements, taken one by one.
+typedef uint32_t raw_even __attribute__((ext_vector_type(4)));
+typedef uint32_t raw_odd __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool BF16>
+struct Raw {
+    raw_even r[BF16 ? 1 : 2];         // eight elements as they are in memory
+};
+
+template <bool BF16, bool EVEN>
+__device__ __forceinline__ Raw<BF16> load_raw(const uint8_t* p, int64_t i, int valid = 8) {
+    Raw<BF16> x;
+    p += i * (BF16 ? 2 : 4);
+    if (EVEN) {
+        x.r[0] = *reinterpret_cast<const raw_even*>(p);
+        if constexpr (!BF16) x.r[1] = *reinterpret_cast<const raw_even*>(p + 16);
+    } else if (valid >= 8) {
+        x.r[0] = *reinterpret_cast<const raw_odd*>(p);
+        if constexpr (!BF16) x.r[1] = *reinterpret_cast<const raw_odd*>(p + 16);
+    } else {
+        uint32_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < 7; ++u)
+            if (u < valid) e[u] = BF16 ? reinterpret_cast<const uint16_t*>(p)[u] : reinterpret_cast<const uint32_t*>(p)[u];
+        if constexpr (BF16) {
+            x.r[0] = raw_even{e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16};
+        } else {
+            x.r[0] = raw_even{e[0], e[1], e[2], e[3]};
+            x.r[1] = raw_even{e[4], e[5], e[6], e[7]};
+        }
+    }
+    return x;
+}
+
+// Elements that this launch reads once.
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load_stream(const uint8_t* p) {
+    Raw<BF16> x;
+    x.r[0] = __builtin_nontemporal_load(reinterpret_cast<const raw_even*>(p));
+    if constexpr (!BF16) x.r[1] = __builtin_nontemporal_load(reinterpret_cast<const raw_even*>(p + 16));
+    return x;
 }
 
 template <bool BF16>
-__device__ __forceinline__ void unpack(const float4* raw, float* v) {
-    const float f[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
-    if constexpr (BF16) {
+__device__ __forceinline__ void unpack(const Raw<BF16>& x, float* v) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(__float_as_uint(f[j]) << 16);
-            v[2 * j + 1] = __uint_as_float(__float_as_uint(f[j]) & 0xffff0000u);
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16) {
+            v[2 * j] = __uint_as_float(x.r[0][j] << 16);
+            v[2 * j + 1] = __uint_as_float(x.r[0][j] & 0xffff0000u);
+        } else {
+            v[j] = __uint_as_float(x.r[0][j]);
+            v[4 + j] = __uint_as_float(x.r[1][j]);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = f[j];
-        v[4] = raw[1].x, v[5] = raw[1].y, v[6] = raw[1].z, v[7] = raw[1].w;
     }
 }
 
-template <bool BF16, int VEC>
-__device__ __forceinline__ void store_vec(uint8_t* p, int64_t i, const float* v) {
-    if constexpr (VEC == 1) {
-        if (BF16) reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)bf16x2(v[0], v[0]);
-        else reinterpret_cast<float*>(p)[i] = v[0];
-    } else if constexpr (BF16) {
-        *reinterpret_cast<uint4*>(p + i * 2) =
-            uint4{bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
+template <bool BF16, bool EVEN>
+__device__ __forceinline__ void store8(uint8_t* p, int64_t i, int valid, const float* v) {
+    p += i * (BF16 ? 2 : 4);
+    if (EVEN || valid >= 8) {
+        using V = typename std::conditional<EVEN, raw_even, raw_odd>::type;
+        if constexpr (BF16) {
+            *reinterpret_cast<V*>(p) = V{bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
+        } else {
+            *reinterpret_cast<V*>(p) =
+                V{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+            *reinterpret_cast<V*>(p + 16) =
+                V{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+        }
     } else {
-        *reinterpret_cast<float4*>(p + i * 4) = float4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<float4*>(p + i * 4 + 16) = float4{v[4], v[5], v[6], v[7]};
+#pragma unroll
+        for (int u = 0; u < 7; ++u)
+            if (u < valid) {
+                if (BF16) reinterpret_cast<uint16_t*>(p)[u] = (uint16_t)bf16x2(v[u], v[u]);
+                else reinterpret_cast<float*>(p)[u] = v[u];
+            }
     }
 }
 
-// z of row t, columns [col, col + VEC)
-template <bool COMBINE, bool BF16, int VEC>
-__device__ __forceinline__ void load_z(const NormArgs& a, int64_t t, int col, const int32_t* rows, const float* wts,
-                                       float* z) {
-    const int64_t i = t * a.H + col;
-    if constexpr (COMBINE) {
-#pragma unroll
-        for (int u = 0; u < VEC; ++u) z[u] = 0.0f;
-        for (int j = 0; j < a.k + a.shared; ++j) {
-            const int64_t row = j < a.k ? (int64_t)rows[j] : a.T * a.k + t;
-            if (row < 0) continue;
-            const float w = j < a.k ? wts[j] : 1.0f;
-            float v[VEC];
-            load_vec<BF16, VEC>(a.x, row * a.H + col, v);
-#pragma unroll
-            for (int u = 0; u < VEC; ++u) z[u] += w * v[u];
+// The weight's vector at a column, in its own type.
+template <bool EVEN>
+struct Weight {
+    raw_even r[2];
+    __device__ __forceinline__ void load(const NormArgs& a, int col, int valid) {
+        if (a.w_bf16) {
+            r[0] = load_raw<true, EVEN>(a.weight, col, valid).r[0];
+        } else {
+            const Raw<false> f = load_raw<false, EVEN>(a.weight, col, valid);
+            r[0] = f.r[0];
+            r[1] = f.r[1];
         }
-    } else {
-        load_vec<BF16, VEC>(a.x, i, z);
     }
-    if (a.residual != nullptr) {
-        float v[VEC];
-        load_vec<BF16, VEC>(a.residual, i, v);
-#pragma unroll
-        for (int u = 0; u < VEC; ++u) z[u] += v[u];
+    __device__ __forceinline__ void get(const NormArgs& a, float* w) const {
+        if (a.w_bf16) unpack<true>(Raw<true>{{r[0]}}, w);
+        else unpack<false>(Raw<false>{{r[0], r[1]}}, w);
     }
-}
+};
 
 // Writes one vector of a row: z is its sum, r the row's factor.  With q the 16 lanes of a 128-column group
 // call it together.
-template <bool BF16, int VEC>
-__device__ __forceinline__ void finish_vec(const NormArgs& a, int64_t t, int col, const float* z, float r) {
+template <bool BF16, bool EVEN>
+__device__ __forceinline__ void finish8(const NormArgs& a, int64_t t, int col, const float* z, float r,
+                                        const Weight<EVEN>& weight) {
     const int64_t i = t * a.H + col;
-    if (a.sum_out != nullptr) store_vec<BF16, VEC>(a.sum_out, i, z);
+    const int valid = a.H - col;
+    if (a.sum_out != nullptr) store8<BF16, EVEN>(a.sum_out, i, valid, z);
     if (a.y == nullptr && a.q == nullptr) return;
-    float w[VEC], n[VEC];
-    if (a.w_bf16) load_vec<true, VEC>(a.weight, col, w);
-    else load_vec<false, VEC>(a.weight, col, w);
+    float n[8];
+    weight.get(a, n);
 #pragma unroll
-    for (int u = 0; u < VEC; ++u) n[u] = z[u] * r * w[u];
-    if (a.y != nullptr) store_vec<BF16, VEC>(a.y, i, n);
-    if constexpr (BF16 && VEC == 8) {
+    for (int u = 0; u < 8; ++u) n[u] = z[u] * r * n[u];
+    if (a.y != nullptr) store8<BF16, EVEN>(a.y, i, valid, n);
+    if constexpr (BF16 && EVEN) {
         if (a.q != nullptr) {
             // the largest magnitude as an integer maximum of the bit patterns, which keeps a NaN
             uint32_t m = 0;
 #pragma unroll
             for (int u = 0; u < 8; ++u) m = max(m, __float_as_uint(n[u]) & 0x7fffffffu);
-#pragma unroll
-            for (int d = 8; d >= 1; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d, 16));
-            const float s = m == 0 ? 1.0f : __uint_as_float(m) / 448.0f;
+            m = max(m, dpp<0xB1>(m));
+            m = max(m, dpp<0x4E>(m));
+            m = max(m, dpp<0x141>(m));
+            m = max(m, dpp<0x140>(m));
+            // no scale below the smallest normal number: a subnormal one is too coarse to divide by
+            const uint32_t sb = max(__float_as_uint(__uint_as_float(m) / 448.0f), 0x00800000u);
+            const float s = m == 0 ? 1.0f : __uint_as_float(sb);
             const uint32_t lo = e4m3x4(n[0] / s, n[1] / s, n[2] / s, n[3] / s);
             const uint32_t hi = e4m3x4(n[4] / s, n[5] / s, n[6] / s, n[7] / s);
             *reinterpret_cast<uint2*>(a.q + i) = uint2{lo, hi};
@@ -152,9 +196,37 @@ __device__ __forceinline__ void finish_vec(const NormArgs& a, int64_t t, int col
     }
 }
 
+// One vector of z = combine + residual, for the two-pass kernel.
+template <bool COMBINE, bool BF16, bool EVEN>
+__device__ __forceinline__ void load_z(const NormArgs& a, int64_t t, int col, const int32_t* rows, const float* wts,
+                                       float* z) {
+    const int64_t i = t * a.H + col;
+    const int valid = a.H - col;
+    float v[8];
+    if constexpr (COMBINE) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) z[u] = 0.0f;
+        for (int j = 0; j < a.k + a.shared; ++j) {
+            const int64_t row = j < a.k ? (int64_t)rows[j] : a.T * a.k + t;
+            if (row < 0) continue;
+            const float w = j < a.k ? wts[j] : 1.0f;
+            unpack<BF16>(load_raw<BF16, EVEN>(a.x, row * a.H + col), v);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) z[u] += w * v[u];
+        }
+    } else {
+        unpack<BF16>(load_raw<BF16, EVEN>(a.x, i, valid), z);
+    }
+    if (a.residual != nullptr) {
+        unpack<BF16>(load_raw<BF16, EVEN>(a.residual, i, valid), v);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) z[u] += v[u];
+    }
+}
+
 // Any width: one workgroup per row, which reads z twice (for the sum of squares, then to write), each
 // element by the same thread, so that outputs may take their inputs' place.
-template <bool COMBINE, bool BF16, int VEC>
+template <bool COMBINE, bool BF16, bool EVEN>
 __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
     __shared__ int32_t s_row[kMaxK];
     __shared__ float s_w[kMaxK];
@@ -168,88 +240,86 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
             s_w[tid] = a.topk_w[t * a.k + tid];
         }
         __syncthreads();
-        float ss = 0.0f, z[VEC];
-        for (int c = tid * VEC; c < a.H; c += 256 * VEC) {
-            load_z<COMBINE, BF16, VEC>(a, t, c, s_row, s_w, z);
+        float ss = 0.0f, z[8];
+        for (int c = tid * 8; c < a.H; c += 256 * 8) {
+            load_z<COMBINE, BF16, EVEN>(a, t, c, s_row, s_w, z);
 #pragma unroll
-            for (int u = 0; u < VEC; ++u) ss += z[u] * z[u];
+            for (int u = 0; u < 8; ++u) ss += z[u] * z[u];
         }
-#pragma unroll
-        for (int d = 32; d >= 1; d >>= 1) ss += __shfl_xor(ss, d);
+        ss = row_sum<64>(ss);
         if ((tid & 63) == 0) s_part[tid >> 6] = ss;
         __syncthreads();
         ss = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
         const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
-        for (int c = tid * VEC; c < a.H; c += 256 * VEC) {
-            load_z<COMBINE, BF16, VEC>(a, t, c, s_row, s_w, z);
-            finish_vec<BF16, VEC>(a, t, c, z, r);
+        for (int c = tid * 8; c < a.H; c += 256 * 8) {
+            load_z<COMBINE, BF16, EVEN>(a, t, c, s_row, s_w, z);
+            Weight<EVEN> w;
+            if (a.weight != nullptr) w.load(a, c, a.H - c);
+            finish8<BF16, EVEN>(a, t, c, z, r, w);
         }
     }
 }
 
 // ------------------------------------------------------------------------------ rows held in registers
 // A thread keeps C vectors of its row (vector c of thread i: c * blockDim.x + i) as fp32 from the one read of
-// the inputs to the one write of the outputs.  blockDim.x threads share a row; rows of one wave need no LDS
-// and are packed blockDim.y to a workgroup.  Loads past the row's end read its last vector instead, so that
-// every lane of a wave stays active up to the sum (lanes read each other's registers on the way).
-
-// Sum over the wave, the same in every lane: four exchanges inside rows of 16 lanes, then the four rows.
-__device__ __forceinline__ float wave_sum(float v) {
-#define DWDP_DPP_ADD(ctrl)                                                                                         \
-    v += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), ctrl, 0xf, 0xf, true))
-    DWDP_DPP_ADD(0xB1);        // lanes 1 apart
-    DWDP_DPP_ADD(0x4E);        // 2 apart
-    DWDP_DPP_ADD(0x141);       // mirrored in 8
-    DWDP_DPP_ADD(0x140);       // mirrored in 16
-#undef DWDP_DPP_ADD
-    const int b = __float_as_int(v);
-    return (__int_as_float(__builtin_amdgcn_readlane(b, 0)) + __int_as_float(__builtin_amdgcn_readlane(b, 16))) +
-           (__int_as_float(__builtin_amdgcn_readlane(b, 32)) + __int_as_float(__builtin_amdgcn_readlane(b, 48)));
-}
-
-template <bool COMBINE, bool BF16, int VEC, int C>
+// the inputs to the one write of the outputs.  blockDim.x threads share a row, LANES of them in one wave; rows of
+// one wave or less need no LDS and are packed blockDim.y to a workgroup.  Loads past the row's end read its
+// last vector instead (combine) or nothing, so that every lane of a wave stays active up to the sum.
+template <bool COMBINE, bool BF16, bool EVEN, int C, int LANES>
 __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
+    static_assert(!COMBINE || EVEN, "combine takes rows of a multiple of 8");
     __shared__ float s_part[16];
-    const int tx = threadIdx.x, bx = blockDim.x, lane = tx & 63;
-    const int n_waves = bx >> 6;
-    for (int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; t < a.T; t += (int64_t)gridDim.x * blockDim.y) {
-        float z[C][VEC];
+    const int tx = threadIdx.x, bx = LANES < 64 ? LANES : blockDim.x, lane = tx & 63;
+    const int n_waves = LANES < 64 ? 1 : bx >> 6;
+    // a row of whole waves has a number that is the same in all lanes: kept in scalar registers
+    const int y = LANES == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.y) : threadIdx.y;
+    const int64_t t0 = (int64_t)blockIdx.x * blockDim.y + y, stride = (int64_t)gridDim.x * blockDim.y;
+    for (int64_t t = t0; t < a.T; t += stride) {
+        float z[C][8];
         if constexpr (COMBINE) {
-            // lane j holds slot j's row and weight (k <= 64); rows out of range are dropped
             const int64_t rows = a.T * (a.k + a.shared);
+            const int nsrc = a.k + a.shared;
+            // rows of a whole wave: lane j holds slot j's row and weight (k <= 64); rows out of range are dropped
             int my_row = -1;
             float my_w = 0.0f;
-            if (lane < a.k) {
+            if (LANES == 64 && lane < a.k) {
                 my_row = a.inv_perm[t * a.k + lane];
                 my_w = a.topk_w[t * a.k + lane];
                 if (my_row >= rows) my_row = -1;
             }
-            const int nsrc = a.k + a.shared;
-            constexpr int B = BF16 ? 16 : 8;              // source rows whose loads are in flight together
+            const int shared_row = (int)(a.T * a.k + t);
+            auto row_of = [&](int j) {
+                if (j >= a.k) return shared_row;
+                if (LANES == 64) return (int)__builtin_amdgcn_readlane(my_row, j);
+                const int r = a.inv_perm[t * a.k + j];
+                return r < rows ? r : -1;
+            };
+            auto weight_of = [&](int j) {
+                if (j >= a.k) return 1.0f;
+                return LANES == 64 ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_w), j)) : a.topk_w[t * a.k + j];
+            };
+            constexpr int B = BF16 ? 10 : 5;              // source rows whose loads are in flight together
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int col = min((c * bx + tx) * VEC, a.H - VEC);
+                const int col = min((c * bx + tx) * 8, a.H - 8);
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) z[c][u] = 0.0f;
+                for (int u = 0; u < 8; ++u) z[c][u] = 0.0f;
                 for (int j0 = 0; j0 < nsrc; j0 += B) {
-                    float4 raw[B][BF16 ? 1 : 2];
+                    // all loads of the batch first (a dropped slot loads row 0 and is skipped below) ...
+                    Raw<BF16> raw[B];
 #pragma unroll
-                    for (int u = 0; u < B; ++u) {
-                        const int j = j0 + u;
-                        if (j < nsrc) {
-                            const int r = j < a.k ? __builtin_amdgcn_readlane(my_row, j) : 0;
-                            const int64_t row = j < a.k ? (r >= 0 ? r : 0) : a.T * a.k + t;
-                            const uint8_t* p = a.x + (row * a.H + col) * (BF16 ? 2 : 4);
-                            raw[u][0] = load_stream(p);
-                            if constexpr (!BF16) raw[u][1] = load_stream(p + 16);
+                    for (int u = 0; u < B; ++u)
+                        if (j0 + u < nsrc) {
+                            const int r = row_of(j0 + u);
+                            const uint8_t* const base = a.x + (int64_t)(r >= 0 ? r : 0) * a.H * (BF16 ? 2 : 4);
+                            raw[u] = load_stream<BF16>(base + (uint32_t)col * (BF16 ? 2u : 4u));
                         }
-                    }
+                    // ... then the sums, in slot order
 #pragma unroll
                     for (int u = 0; u < B; ++u) {
                         const int j = j0 + u;
-                        if (j >= nsrc || (j < a.k && __builtin_amdgcn_readlane(my_row, j) < 0)) continue;
-                        const float w =
-                            j < a.k ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(my_w), j)) : 1.0f;
+                        if (j >= nsrc || row_of(j) < 0) continue;
+                        const float w = weight_of(j);
                         float v[8];
                         unpack<BF16>(raw[u], v);
 #pragma unroll
@@ -259,27 +329,46 @@ __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                load_vec<BF16, VEC>(a.x, t * a.H + min((c * bx + tx) * VEC, a.H - VEC), z[c]);
+            for (int c = 0; c < C; ++c) {
+                const int col = (c * bx + tx) * 8;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) z[c][u] = 0.0f;
+                if (col < a.H) unpack<BF16>(load_raw<BF16, EVEN>(a.x, t * a.H + col, a.H - col), z[c]);
+            }
         }
         if (a.residual != nullptr) {
-            float v[C][VEC];
+            Raw<BF16> res[C];
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                load_vec<BF16, VEC>(a.residual, t * a.H + min((c * bx + tx) * VEC, a.H - VEC), v[c]);
+            for (int c = 0; c < C; ++c) {
+                const int col = (c * bx + tx) * 8;
+                if (col < a.H) res[c] = load_raw<BF16, EVEN>(a.residual, t * a.H + col, a.H - col);
+            }
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int c = 0; c < C; ++c) {
+                float v[8];
+                unpack<BF16>(res[c], v);
 #pragma unroll
-                for (int u = 0; u < VEC; ++u) z[c][u] += v[c][u];
+                for (int u = 0; u < 8; ++u) z[c][u] += v[u];
+            }
+        }
+        // the weight is on its way while the row is summed, where registers allow it
+        constexpr bool EARLY = C == 1;
+        Weight<EVEN> weight[EARLY ? C : 1];
+        if (EARLY && a.weight != nullptr) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int col = (c * bx + tx) * 8;
+                if (col < a.H) weight[EARLY ? c : 0].load(a, col, a.H - col);
+            }
         }
         float ss = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const bool in = (c * bx + tx) * VEC < a.H;
+            const bool in = (c * bx + tx) * 8 < a.H;
 #pragma unroll
-            for (int u = 0; u < VEC; ++u) ss += in ? z[c][u] * z[c][u] : 0.0f;
+            for (int u = 0; u < 8; ++u) ss += in ? z[c][u] * z[c][u] : 0.0f;
         }
-        ss = wave_sum(ss);
+        ss = row_sum<LANES>(ss);
         if (n_waves > 1) {
             if (lane == 0) s_part[tx >> 6] = ss;
             __syncthreads();
@@ -290,43 +379,52 @@ __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
         const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int col = (c * bx + tx) * VEC;
-            if (col < a.H) finish_vec<BF16, VEC>(a, t, col, z[c], r);
+            const int col = (c * bx + tx) * 8;
+            if (col < a.H) {
+                if (!EARLY && a.weight != nullptr) weight[0].load(a, col, a.H - col);
+                finish8<BF16, EVEN>(a, t, col, z[c], r, weight[EARLY ? c : 0]);
+            }
         }
     }
 }
 
-template <bool COMBINE, bool BF16, int VEC, int C>
+template <bool COMBINE, bool BF16, bool EVEN, int C, int LANES>
 void launch_rows(const NormArgs& a, int threads, hipStream_t st) {
-    const int rows = threads == 64 ? 4 : 1;
+    const int rows = threads <= 64 ? 256 / threads : 1;
     const unsigned grid = (unsigned)std::min<int64_t>((a.T + rows - 1) / rows, kMaxRowGrid);
-    hipLaunchKernelGGL((norm_row_kernel<COMBINE, BF16, VEC, C>), dim3(grid), dim3(threads, rows), 0, st, a);
+    hipLaunchKernelGGL((norm_row_kernel<COMBINE, BF16, EVEN, C, LANES>), dim3(grid), dim3(threads, rows), 0, st, a);
 }
 
-template <bool COMBINE, bool BF16, int VEC>
+template <bool COMBINE, bool BF16, bool EVEN>
 void launch_typed(const NormArgs& a, hipStream_t st) {
-    // the largest counts that stay in 128 registers (combine: its source rows in flight take the rest)
-    constexpr int C1 = VEC == 8 ? kManyC : 4, C2 = COMBINE ? C1 : VEC == 8 ? 4 : 8;
-    const int64_t nvec = (a.H + VEC - 1) / VEC;
+    const int64_t nvec = ((int64_t)a.H + 7) / 8;
     auto threads = [&](int c) { return (int)(((nvec + c - 1) / c + 63) / 64 * 64); };
-    if (threads(1) <= 64 || (a.T <= kFewRows && threads(1) <= 1024))
-        launch_rows<COMBINE, BF16, VEC, 1>(a, threads(1), st);
-    else if (threads(C1) <= 1024) launch_rows<COMBINE, BF16, VEC, C1>(a, threads(C1), st);
-    else if (C2 != C1 && threads(C2) <= 1024) launch_rows<COMBINE, BF16, VEC, C2>(a, threads(C2), st);
-    else {
+    if (nvec <= 16) {
+        launch_rows<COMBINE, BF16, EVEN, 1, 16>(a, 16, st);
+    } else if (nvec <= 32) {
+        launch_rows<COMBINE, BF16, EVEN, 1, 32>(a, 32, st);
+    } else if (nvec <= 64 || (a.T <= kFewRows && nvec <= 1024)) {
+        launch_rows<COMBINE, BF16, EVEN, 1, 64>(a, threads(1), st);
+    } else if (nvec <= 2 * 1024) {
+        launch_rows<COMBINE, BF16, EVEN, 2, 64>(a, threads(2), st);
+    } else {
+        // wider rows: four vectors a thread, unless combine's source rows in flight need the registers
+        if constexpr (!COMBINE) {
+            if (nvec <= 4 * 1024) return launch_rows<false, BF16, EVEN, 4, 64>(a, threads(4), st);
+        }
         const dim3 grid((unsigned)std::min<int64_t>(a.T, kMaxRowGrid));
-        hipLaunchKernelGGL((norm_two_pass_kernel<COMBINE, BF16, VEC>), grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL((norm_two_pass_kernel<COMBINE, BF16, EVEN>), grid, dim3(256), 0, st, a);
     }
 }
 
 template <bool COMBINE>
-int launch_norm(const NormArgs& a, bool bf16, bool vec, hipStream_t st) {
-    if (vec) {
-        if (bf16) launch_typed<COMBINE, true, 8>(a, st);
-        else launch_typed<COMBINE, false, 8>(a, st);
+int launch_norm(const NormArgs& a, bool bf16, bool even, hipStream_t st) {
+    if (even) {
+        if (bf16) launch_typed<COMBINE, true, true>(a, st);
+        else launch_typed<COMBINE, false, true>(a, st);
     } else if constexpr (!COMBINE) {
-        if (bf16) launch_typed<false, true, 1>(a, st);
-        else launch_typed<false, false, 1>(a, st);
+        if (bf16) launch_typed<false, true, false>(a, st);
+        else launch_typed<false, false, false>(a, st);
     }
     DWDP_LAUNCHED();
     return DWDP_OK;
@@ -356,9 +454,9 @@ extern "C" int dwdp_add_rmsnorm(const void* x, const void* residual, int dtype, 
     DWDP_REQUIRE(type_aligned(x, eb) && type_aligned(residual, eb) && type_aligned(sum_out, eb) && type_aligned(y, eb) &&
                      type_aligned(weight, elem_bytes(w_dtype)) && type_aligned(q, 8) && type_aligned(q_scale, 4),
                  "a pointer is not aligned to its element type (q: 8 bytes)");
-    const bool vec = H % 8 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(sum_out) &&
+    const bool even = H % 8 == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(sum_out) &&
                      aligned16(y);
-    if (q != nullptr) DWDP_REQUIRE(vec, "q needs 16-byte aligned x, residual, weight, sum_out and y");
+    if (q != nullptr) DWDP_REQUIRE(even, "q needs 16-byte aligned x, residual, weight, sum_out and y");
     NormArgs a{};
     a.x = static_cast<const uint8_t*>(x);
     a.residual = static_cast<const uint8_t*>(residual);
@@ -371,7 +469,7 @@ extern "C" int dwdp_add_rmsnorm(const void* x, const void* residual, int dtype, 
     a.y = static_cast<uint8_t*>(y);
     a.q = static_cast<uint8_t*>(q);
     a.q_scale = q_scale;
-    return launch_norm<false>(a, dtype == DWDP_BF16, vec, as_stream(stream));
+    return launch_norm<false>(a, dtype == DWDP_BF16, even, as_stream(stream));
 }
 
 extern "C" int dwdp_combine_add_rmsnorm(const void* y_perm, const int32_t* inv_perm, const float* topk_w, int64_t T,

@@ -731,3 +731,33 @@ def test_a_stream_and_its_tensors():
         device_index, cuda_stream = 7, 0
     with pytest.raises(ValueError, match="belongs to GPU 7"):
         api.add_rmsnorm(x, None, x[0], 1e-6, y=torch.empty_like(x), stream=Other())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(1, 9), (7, 15), (130, 17), (67, 129), (40, 263), (33, 511), (600, 513), (9, 2055), (514, 4100), (3, 7161), (4, 16383),
+                                 (2, 32767)])
+def test_add_rmsnorm_of_widths_no_vector_divides(T, H, dt):
+    """The last elements of a row are read and written one by one, and the rows start at odd addresses."""
+    from split_weight_expert_amd import api
+    x, r, w = norm_case(T, H, dt, T * H)
+    for residual in (r, None):
+        z = x.double().cpu().numpy() + (0 if residual is None else r.double().cpu().numpy())
+        so, y = guarded(T, H, DT[dt]), guarded(T, H, DT[dt])
+        api.add_rmsnorm(x, residual, w, 1e-6, so[:T], y[:T])
+        torch.cuda.synchronize()
+        assert (so[T:] == 77).all() and (y[T:] == 77).all(), "rows behind the last were written"
+        check_norm(z, U32 * np.abs(z), w.double().cpu().numpy(), 1e-6, dt, so[:T], y[:T])
+
+
+def test_scales_of_tiny_rows_stay_normal():
+    """amax / 448 below the smallest normal number: the scale is that number, and the codes are finite."""
+    from split_weight_expert_amd import api
+    T, H = 6, 256
+    x = torch.ones(T, H, device=DEV, dtype=torch.bfloat16)
+    w = torch.full((H,), 2.0 ** -126, device=DEV)
+    w[128:] = 2.0 ** -140
+    q, qs = torch.empty(T, H, dtype=torch.uint8, device=DEV), torch.empty(T, H // 128, device=DEV)
+    api.add_rmsnorm(x, None, w, 0.0, q=q, q_scale=qs)
+    assert (qs == 2.0 ** -126).all()
+    c = codecs.e4m3_decode(q.cpu().numpy())
+    assert (c[:, :128] == 1).all() and (c[:, 128:] == 0).all()
