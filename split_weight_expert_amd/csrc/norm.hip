@@ -142,36 +142,17 @@ __device__ __forceinline__ void store8(uint8_t* p, int64_t i, int valid, const f
     }
 }
 
-// The weight's vector at a column, in its own type.
-template <bool EVEN>
-struct Weight {
-    raw_even r[2];
-    __device__ __forceinline__ void load(const NormArgs& a, int col, int valid) {
-        if (a.w_bf16) {
-            r[0] = load_raw<true, EVEN>(a.weight, col, valid).r[0];
-        } else {
-            const Raw<false> f = load_raw<false, EVEN>(a.weight, col, valid);
-            r[0] = f.r[0];
-            r[1] = f.r[1];
-        }
-    }
-    __device__ __forceinline__ void get(const NormArgs& a, float* w) const {
-        if (a.w_bf16) unpack<true>(Raw<true>{{r[0]}}, w);
-        else unpack<false>(Raw<false>{{r[0], r[1]}}, w);
-    }
-};
-
 // Writes one vector of a row: z is its sum, r the row's factor.  With q the 16 lanes of a 128-column group
 // call it together.
 template <bool BF16, bool EVEN>
-__device__ __forceinline__ void finish8(const NormArgs& a, int64_t t, int col, const float* z, float r,
-                                        const Weight<EVEN>& weight) {
+__device__ __forceinline__ void finish8(const NormArgs& a, int64_t t, int col, const float* z, float r) {
     const int64_t i = t * a.H + col;
     const int valid = a.H - col;
     if (a.sum_out != nullptr) store8<BF16, EVEN>(a.sum_out, i, valid, z);
     if (a.y == nullptr && a.q == nullptr) return;
     float n[8];
-    weight.get(a, n);
+    if (a.w_bf16) unpack<true>(load_raw<true, EVEN>(a.weight, col, valid), n);
+    else unpack<false>(load_raw<false, EVEN>(a.weight, col, valid), n);
 #pragma unroll
     for (int u = 0; u < 8; ++u) n[u] = z[u] * r * n[u];
     if (a.y != nullptr) store8<BF16, EVEN>(a.y, i, valid, n);
@@ -253,9 +234,7 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
         const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
         for (int c = tid * 8; c < a.H; c += 256 * 8) {
             load_z<COMBINE, BF16, EVEN>(a, t, c, s_row, s_w, z);
-            Weight<EVEN> w;
-            if (a.weight != nullptr) w.load(a, c, a.H - c);
-            finish8<BF16, EVEN>(a, t, c, z, r, w);
+            finish8<BF16, EVEN>(a, t, c, z, r);
         }
     }
 }
@@ -351,16 +330,6 @@ __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
                 for (int u = 0; u < 8; ++u) z[c][u] += v[u];
             }
         }
-        // the weight is on its way while the row is summed, where registers allow it
-        constexpr bool EARLY = C == 1;
-        Weight<EVEN> weight[EARLY ? C : 1];
-        if (EARLY && a.weight != nullptr) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int col = (c * bx + tx) * 8;
-                if (col < a.H) weight[EARLY ? c : 0].load(a, col, a.H - col);
-            }
-        }
         float ss = 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -380,10 +349,7 @@ __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = (c * bx + tx) * 8;
-            if (col < a.H) {
-                if (!EARLY && a.weight != nullptr) weight[0].load(a, col, a.H - col);
-                finish8<BF16, EVEN>(a, t, col, z[c], r, weight[EARLY ? c : 0]);
-            }
+            if (col < a.H) finish8<BF16, EVEN>(a, t, col, z[c], r);
         }
     }
 }
