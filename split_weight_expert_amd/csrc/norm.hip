@@ -14,7 +14,6 @@ namespace dwdp {
 namespace {
 
 constexpr int kMaxK = 64;
-constexpr int kFewRows = 512;
 
 struct NormArgs {
     // z's source
@@ -365,11 +364,16 @@ template <bool COMBINE, bool BF16, bool EVEN>
 void launch_typed(const NormArgs& a, hipStream_t st) {
     const int64_t nvec = ((int64_t)a.H + 7) / 8;
     auto threads = [&](int c) { return (int)(((nvec + c - 1) / c + 63) / 64 * 64); };
+    // One vector a thread as long as all rows' waves find a place on the chip at once (16 on each of 256 compute
+    // units), two beyond: combine of 7168-wide rows, k = 8 and a shared row: 256 tokens 9.6 against 10.6 us,
+    // 512 tokens 21.1 against 18.4; 2048-wide: 1024 tokens 10.2 against 11.7, 4096 37.5 against 40.4 (norm alone:
+    // 15.4 against 14.7).
+    const bool few = a.T * (threads(1) / 64) <= 4096;
     if (nvec <= 16) {
         launch_rows<COMBINE, BF16, EVEN, 1, 16>(a, 16, st);
     } else if (nvec <= 32) {
         launch_rows<COMBINE, BF16, EVEN, 1, 32>(a, 32, st);
-    } else if (nvec <= 64 || (a.T <= kFewRows && nvec <= 1024)) {
+    } else if (nvec <= 64 || (few && nvec <= 1024)) {
         launch_rows<COMBINE, BF16, EVEN, 1, 64>(a, threads(1), st);
     } else if (nvec <= 2 * 1024) {
         launch_rows<COMBINE, BF16, EVEN, 2, 64>(a, threads(2), st);
