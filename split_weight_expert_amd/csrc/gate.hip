@@ -334,6 +334,10 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         }
     };
     constexpr unsigned long long kToken = L == 64 ? ~0ull : (1ull << (L & 63)) - 1;
+    // Lanes read each other's logits from memory; with a sliced product this wave has just written them.
+    auto logits_written = [&] {
+        if constexpr (SLICED) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    };
     // The softmax's denominator and an expert's choice in fp64, for close calls.  m: the largest logit.
     auto softmax_total = [&](int64_t t, float m) {
         double s = 0.0;
@@ -386,8 +390,6 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
                 for (int i = 0; i < PL; ++i)
                     if (i < count) out[i] = l[i];
             }
-            // lanes of this wave read each other's logits below
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
         } else {
             load(a.logits + t * a.E + base, l);
         }
@@ -464,6 +466,7 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
             unsure = need_scores && last && next > f_neg_inf() && !(value - next >= margin);
             const unsigned long long who = __ballot(unsure);
             if (who != 0) {
+                logits_written();
                 // the same by fp64 values of each group's two best; where a third expert is so near that it may be
                 // one of them, in a group near the border, the token stays unsure
                 const float border = over_token<L>(last ? value : f_neg_inf(), MaxF());
@@ -517,6 +520,7 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         }
         bool has = q < a.k && !gone(picked);
         int my_i = gone(picked) ? 0 : key_expert(picked);
+        logits_written();
         if (__ballot(close) != 0) {
             // prev is the best expert that is no candidate
             const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
