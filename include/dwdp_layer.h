@@ -65,7 +65,9 @@ typedef struct {
  *   logits_out [T,E] fp32 (written, bias included), topk_idx [T,k] int32, topk_w [T,k] fp32.
  *   ws: dwdp_route_gate_workspace_bytes(...) bytes of device scratch, 16-byte aligned (NULL if 0); its
  *   contents need no preparation and mean nothing after the call.  Calls that may run at the same time
- *   need a workspace each. */
+ *   need a workspace each.
+ *   No output, nor ws, may overlap another buffer.  T is limited by one launch of the product (bf16: 10^9
+ *   tokens and more; f32: about 8 million tokens of 256 experts); larger ones are refused. */
 int dwdp_route_gate(const void* x, const void* w_router, int in_dtype, const float* bias,
                     const float* balance_bias, int64_t T, int H, int E, const dwdp_gate* gate,
                     float* logits_out, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,
@@ -74,7 +76,7 @@ int dwdp_route_gate(const void* x, const void* w_router, int in_dtype, const flo
 /* Device scratch dwdp_route_gate needs (0 where it needs none, and for arguments it rejects). */
 size_t dwdp_route_gate_workspace_bytes(int64_t T, int H, int E, int in_dtype);
 
-/* The gate alone: logits [T,E] fp32 -> topk_idx [T,k], topk_w [T,k]. */
+/* The gate alone: logits [T,E] fp32 -> topk_idx [T,k], topk_w [T,k], neither of which may overlap another buffer. */
 int dwdp_gate_topk(const float* logits, const float* balance_bias, int64_t T, int E, const dwdp_gate* gate,
                    int32_t* topk_idx, float* topk_w, void* stream);
 
@@ -85,17 +87,17 @@ int dwdp_gate_topk(const float* logits, const float* balance_bias, int64_t T, in
  *   y = n rounded to dtype                                         (NULL: not written)
  *   q, q_scale = n quantised like dwdp_quantize_tokens_fp8 quantises a row, from the unrounded n: per
  *   128 columns scale = amax/448 (1 when amax is 0, 2^-126 where amax/448 is less), code = E4M3(n/scale)
-   (NULL, both: not written)
+ *   (NULL, both: not written)
  * At least one of y and q is given.  Non-finite values follow IEEE arithmetic; a NaN in a 128-column
  * group makes its scale and its codes NaN.  z^2 is summed in fp32: rows whose sum of squares passes
- * 3.4e38 norm to zero.
+ * 3.4e38 norm to zero, and with eps 0 a row whose squares all underflow norms to infinities and NaN.
  *   x, residual, sum_out, y [T,H] of dtype (DWDP_F32 or DWDP_BF16); weight [H] of w_dtype (DWDP_F32 or
  *   DWDP_BF16).  Any H >= 1 and any element-aligned pointers; rows are read fastest where
  *   H % 8 == 0 and all pointers are 16-byte aligned.  q [T,H] (8-byte aligned) with q_scale [T,H/128]
  *   fp32 needs dtype DWDP_BF16, H % 128 == 0 and 16-byte aligned x, residual, weight, sum_out and y.
  *   eps >= 0, finite.
  *   In place: sum_out and y may each be x or residual (the same address), but not each other; other
- *   overlaps are not allowed. */
+ *   overlaps of an output with any buffer are refused. */
 int dwdp_add_rmsnorm(const void* x, const void* residual, int dtype, const void* weight, int w_dtype, float eps,
                      int64_t T, int H, void* sum_out, void* y, void* q, float* q_scale, void* stream);
 
@@ -107,7 +109,8 @@ int dwdp_add_rmsnorm(const void* x, const void* residual, int dtype, const void*
  * y and q is given.
  *   T >= 0, T*(k + shared) < 2^31, 1 <= k <= 64, H % 8 == 0 (H % 128 == 0 and DWDP_BF16 with q); y_perm [T*k + shared*T, H],
  *   residual, sum_out, y [T,H] of dtype, weight [H] of w_dtype, all 16-byte aligned (q: 8-byte).
- *   In place: sum_out or y may be residual; y_perm overlaps no output. */
+ *   In place: sum_out or y may be residual (the same address); other overlaps of an output with any buffer
+ *   are refused. */
 int dwdp_combine_add_rmsnorm(const void* y_perm, const int32_t* inv_perm, const float* topk_w, int64_t T, int k,
                              int shared, int H, int dtype, const void* residual, const void* weight, int w_dtype,
                              float eps, void* sum_out, void* y, void* q, float* q_scale, void* stream);

@@ -210,6 +210,8 @@ class Gate:
     def __post_init__(self):
         if self.score not in _SCORES:
             raise ValueError(f"score must be one of {sorted(_SCORES)}, not {self.score!r}")
+        if any(not -1 << 31 <= v < 1 << 31 for v in (self.k, self.n_groups, self.topk_groups, self.group_top)):
+            raise ValueError("k, n_groups, topk_groups and group_top are 32-bit numbers")
         c = _lib.GateArgs(_SCORES[self.score], self.k, self.n_groups, self.topk_groups, self.group_top,
                           int(self.renormalize), self.scale)
         object.__setattr__(self, "_c", c)
@@ -249,6 +251,8 @@ def _raw_stream(stream, index):
 def _matrix(name, t):
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, not {t.dim()}")
+    if t.shape[1] >= 1 << 31:                 # widths are 32-bit numbers in the library
+        raise ValueError(f"{name} has too many columns")
     return t.shape
 
 

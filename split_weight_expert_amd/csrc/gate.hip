@@ -569,22 +569,22 @@ bool aligned4(const void* a, const void* b, const void* c, const void* d, const 
 }
 
 int check_gate(const char* fn, const dwdp_gate* g, int E) {
-    const std::string f = std::string(fn) + ": ";
-    if (g == nullptr) return fail(DWDP_ERR_INVALID_ARG, f + "gate is NULL");
-    if (E < 1 || E > kMaxE) return fail(DWDP_ERR_INVALID_ARG, f + "E must be in [1, 1024]");
+    auto bad = [&](const char* what) { return fail(DWDP_ERR_INVALID_ARG, std::string(fn) + ": " + what); };
+    if (g == nullptr) return bad("gate is NULL");
+    if (E < 1 || E > kMaxE) return bad("E must be in [1, 1024]");
     if (g->score != DWDP_SCORE_SOFTMAX && g->score != DWDP_SCORE_SIGMOID)
-        return fail(DWDP_ERR_INVALID_ARG, f + "score must be DWDP_SCORE_SOFTMAX or DWDP_SCORE_SIGMOID");
-    if (g->k < 1 || g->k > E || g->k > kMaxK) return fail(DWDP_ERR_INVALID_ARG, f + "k must be in [1, min(E, 32)]");
+        return bad("score must be DWDP_SCORE_SOFTMAX or DWDP_SCORE_SIGMOID");
+    if (g->k < 1 || g->k > E || g->k > kMaxK) return bad("k must be in [1, min(E, 32)]");
     if (g->n_groups < 1 || g->n_groups > E || E % g->n_groups != 0)
-        return fail(DWDP_ERR_INVALID_ARG, f + "n_groups must divide E");
+        return bad("n_groups must divide E");
     if (g->topk_groups < 1 || g->topk_groups > g->n_groups)
-        return fail(DWDP_ERR_INVALID_ARG, f + "topk_groups must be in [1, n_groups]");
+        return bad("topk_groups must be in [1, n_groups]");
     if (g->k > g->topk_groups * (E / g->n_groups))
-        return fail(DWDP_ERR_INVALID_ARG, f + "k must be at most the experts of topk_groups groups");
-    if (g->group_top != 1 && g->group_top != 2) return fail(DWDP_ERR_INVALID_ARG, f + "group_top must be 1 or 2");
+        return bad("k must be at most the experts of topk_groups groups");
+    if (g->group_top != 1 && g->group_top != 2) return bad("group_top must be 1 or 2");
     if (g->renormalize != 0 && g->renormalize != 1)
-        return fail(DWDP_ERR_INVALID_ARG, f + "renormalize must be 0 or 1");
-    if (!std::isfinite(g->scale)) return fail(DWDP_ERR_INVALID_ARG, f + "scale must be finite");
+        return bad("renormalize must be 0 or 1");
+    if (!std::isfinite(g->scale)) return bad("scale must be finite");
     return DWDP_OK;
 }
 
@@ -682,6 +682,10 @@ extern "C" int dwdp_gate_topk(const float* logits, const float* balance_bias, in
     if (T == 0) return DWDP_OK;
     DWDP_REQUIRE(logits && topk_idx && topk_w, "null pointer argument");
     DWDP_REQUIRE(aligned4(logits, balance_bias, topk_idx, topk_w), "a pointer is not aligned to 4 bytes");
+    const size_t chosen = (size_t)T * gate->k * 4;
+    const Span outs[] = {{topk_idx, chosen}, {topk_w, chosen}};
+    const Span ins[] = {{logits, (size_t)T * E * 4}, {balance_bias, (size_t)E * 4}};
+    DWDP_REQUIRE(!overlap_any(outs, 2, ins, 2), "an output overlaps another buffer");
     return launch_gate(gate_args(logits, balance_bias, T, E, *gate, topk_idx, topk_w), as_stream(stream));
 }
 
@@ -714,9 +718,14 @@ extern "C" int dwdp_route_gate(const void* x, const void* w_router, int in_dtype
         DWDP_REQUIRE(ws != nullptr && aligned16(ws), "ws is NULL or not 16-byte aligned");
         if (ws_bytes < need) return fail(DWDP_ERR_WORKSPACE, "dwdp_route_gate: workspace too small");
     }
+    const RouterPlan p = plan_router(T, H, E, in_dtype);
+    DWDP_REQUIRE(router_fits(T, E, p), "T too large for one router launch");
+    const size_t chosen = (size_t)T * gate->k * 4, row = (size_t)H * elem_bytes(in_dtype);
+    const Span outs[] = {{logits_out, (size_t)T * E * 4}, {topk_idx, chosen}, {topk_w, chosen}, {ws, need}};
+    const Span ins[] = {{x, T * row}, {w_router, E * row}, {bias, (size_t)E * 4}, {balance_bias, (size_t)E * 4}};
+    DWDP_REQUIRE(!overlap_any(outs, 4, ins, 4), "an output or ws overlaps another buffer");
     hipStream_t st = as_stream(stream);
     GateArgs a = gate_args(logits_out, balance_bias, T, E, *gate, topk_idx, topk_w);
-    const RouterPlan p = plan_router(T, H, E, in_dtype);
     if (p.slices > 1 && lanes_hold(a)) {
         a.part = static_cast<const float*>(ws);
         a.bias = bias;

@@ -387,6 +387,20 @@ void launch_typed(const NormArgs& a, hipStream_t st) {
     }
 }
 
+// Outputs against every other buffer; sum_out and y may take the place of a row input (x of add, residual).
+bool outputs_are_apart(const NormArgs& a, size_t eb, bool combine) {
+    const size_t rows = (size_t)a.T * a.H, slots = (size_t)a.T * a.k * 4;
+    const Span outs[] = {{a.sum_out, rows * eb}, {a.y, rows * eb}, {a.q, rows}, {a.q_scale, rows / kFp8Group * 4}};
+    const Span fixed[] = {{a.weight, (size_t)a.H * (a.w_bf16 ? 2 : 4)}, {a.inv_perm, slots}, {a.topk_w, slots},
+                          {combine ? a.x : nullptr, rows * eb * (a.k + a.shared)}};
+    if (overlap_any(outs, 4, fixed, 4)) return false;
+    const Span in_place[] = {{combine ? nullptr : a.x, rows * eb}, {a.residual, rows * eb}};
+    for (int i = 0; i < 4; ++i)
+        for (const Span& in : in_place)
+            if (overlap(outs[i], in) && !(i < 2 && outs[i].p == in.p)) return false;
+    return true;
+}
+
 template <bool COMBINE>
 int launch_norm(const NormArgs& a, bool bf16, bool even, hipStream_t st) {
     if (even) {
@@ -439,6 +453,7 @@ extern "C" int dwdp_add_rmsnorm(const void* x, const void* residual, int dtype, 
     a.y = static_cast<uint8_t*>(y);
     a.q = static_cast<uint8_t*>(q);
     a.q_scale = q_scale;
+    DWDP_REQUIRE(outputs_are_apart(a, eb, false), "an output overlaps another buffer");
     return launch_norm<false>(a, dtype == DWDP_BF16, even, as_stream(stream));
 }
 
@@ -481,5 +496,6 @@ extern "C" int dwdp_combine_add_rmsnorm(const void* y_perm, const int32_t* inv_p
     a.y = static_cast<uint8_t*>(y);
     a.q = static_cast<uint8_t*>(q);
     a.q_scale = q_scale;
+    DWDP_REQUIRE(outputs_are_apart(a, elem_bytes(dtype), true), "an output overlaps another buffer");
     return launch_norm<true>(a, dtype == DWDP_BF16, true, as_stream(stream));
 }

@@ -12,7 +12,11 @@ struct RouterPlan {
 };
 RouterPlan plan_router(int64_t T, int H, int E, int dtype);
 
-// logits (one slice) or part[slice][T][E] (more) = x w^T; arguments are checked, T >= 1.
+// Whether one launch holds the plan's tiles.
+bool router_fits(int64_t T, int E, const RouterPlan& p);
+
+// logits (one slice) or part[slice][T][E] (more) = x w^T; arguments are checked, T >= 1,
+// and the plan fits.
 int router_split(const void* x, const void* w, int dtype, const float* bias, int64_t T, int H, int E, const RouterPlan& p,
                  float* logits, float* part, hipStream_t st);
 

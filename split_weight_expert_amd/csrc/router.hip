@@ -248,6 +248,11 @@ RouterPlan plan_router(int64_t T, int H, int E, int dtype) {
     return p;
 }
 
+bool router_fits(int64_t T, int E, const RouterPlan& p) {
+    const int64_t tiles = ceil_div(T, p.bm) * ceil_div(E, p.bn) * p.slices;
+    return (tiles + kNumXcd) * 512 <= kMaxLaunchItems;
+}
+
 int router_split(const void* x, const void* w, int dtype, const float* bias, int64_t T, int H, int E, const RouterPlan& p,
                  float* logits, float* part, hipStream_t st) {
     RouterArgs a{};
@@ -262,7 +267,6 @@ int router_split(const void* x, const void* w, int dtype, const float* bias, int
     a.n_tiles = (int)ceil_div(E, p.bn);
     a.out = p.slices == 1 ? logits : part;
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles * a.slices;
-    DWDP_REQUIRE((tiles + kNumXcd) * 512 <= kMaxLaunchItems, "T too large for one router launch");
     if (p.bm == 16) {
         const dim3 grid((unsigned)tiles), block(kFewWaves * 64);
         if (dtype == DWDP_BF16) hipLaunchKernelGGL(router_few_kernel<true>, grid, block, 0, st, a);

@@ -133,6 +133,7 @@ class BlockBuffers:
     x_tokens: torch.Tensor | None = None  # token mode: the rows GEMM1 reads (x, or x_q for fp8)
     ws_route: torch.Tensor | None = None  # workspace of the gate's router product (None: it needs none)
     x_norm: torch.Tensor | None = None    # normed layers: the block's input, written by the norm before it
+    normed: bool = False                  # x_norm (and for fp8 x_q) hold a normed input that no forward() replaced
 
 
 class MoEBlock:
@@ -192,6 +193,7 @@ class MoEBlock:
         api.route_topk(x, w_router, bias, self.k, b.logits, b.idx, b.w, stream)
 
     def permute(self, x, b: BlockBuffers, stream=None):
+        b.normed = False                      # fp8: the codes below take the normed ones' place
         """Expert permutation; gather mode also writes x_perm, token mode quantises the tokens for fp8."""
         fp8 = self.w_dtype == FP8_E4M3
         api.permute(b.idx, self.E, self.shared, x, self.w_dtype if fp8 else api.dtype_code(x),
@@ -233,6 +235,7 @@ class MoEBlock:
     def _norm_outputs(self, b: BlockBuffers):
         if b.x_norm is None:
             b.x_norm = torch.empty_like(b.y)
+        b.normed = True
         return dict(y=b.x_norm, q=b.x_q, q_scale=b.x_q_scale)
 
     def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None):
@@ -244,7 +247,7 @@ class MoEBlock:
         """A layer whose normed input is in the buffers: h + block(b.x_norm) to `out` (b.y if not given; h itself
         works), and with next_weight that sum's norm to the buffers, the next layer's input."""
         b = self.buffers(h.shape[0])
-        if b.x_norm is None:
+        if not b.normed:
             raise ValueError("no normed input: call norm() on the buffers first")
         self.route(b.x_norm, w_router, bias, b, stream, balance_bias)
         api.permute(b.idx, self.E, self.shared, b.x_norm,

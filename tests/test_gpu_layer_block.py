@@ -78,6 +78,32 @@ def test_a_balance_bias_needs_a_gate():
         blk.forward_normed(torch.zeros(4, 256, device=DEV), None, None, None)
 
 
+def test_a_forward_in_between_takes_the_normed_input():
+    """forward() on the same buffers writes the codes that the norm wrote: no later layer may read the mixture."""
+    from split_weight_expert_amd import MoEBlock
+    name, kw = CASES["fp8"]
+    cfg = shrink(synth.get_config(name), **kw)
+    h = HostLayer(cfg)
+    pl = [(0, e) if e < cfg.n_local else (1, e - cfg.n_local) for e in range(cfg.E)] + [(0, cfg.n_local)]
+    store, table, x, wr, b = upload_layer(h, pl, [cfg.n_local + 1, cfg.E - cfg.n_local])
+    blk = MoEBlock(cfg.H, cfg.I, cfg.E, cfg.k, cfg.shared, cfg.dtype, DEV, gate=make_gate(cfg))
+    w = torch.ones(cfg.H, dtype=x.dtype, device=DEV)
+    bb = blk.buffers(cfg.T)
+    blk.norm(x, w, 1e-6, bb)
+    y0 = blk.forward_normed(x, wr, b, table, out=torch.empty_like(x)).x_norm.clone()
+    first = bb.y_perm.clone()
+    blk.forward_normed(x, wr, b, table, out=torch.empty_like(x))       # the input is still there
+    assert torch.equal(bb.y_perm, first)
+    blk.forward(x * 2, wr, b, table)
+    with pytest.raises(ValueError, match="no normed input"):
+        blk.forward_normed(x, wr, b, table)
+    blk.norm(x, w, 1e-6, bb)
+    blk.forward_normed(x, wr, b, table, out=torch.empty_like(x))
+    torch.cuda.synchronize()
+    assert torch.equal(bb.x_norm, y0) and torch.equal(bb.y_perm, first)
+    del store
+
+
 @pytest.mark.parametrize("dt,n_sets", [("f32", 2), ("bf16", 2), ("fp8", 2), ("bf16", 3)])
 def test_pipeline_of_prenorm_layers(dt, n_sets):
     from split_weight_expert_amd import DWDPPipeline, api

@@ -161,6 +161,55 @@ def test_combine_add_rmsnorm_rejects_bad_arguments(lib):
     assert f(T=0, yp=None, ip=None, tw=None, s=None) == 0
 
 
+def _at(base, step=1 << 24):
+    """Distinct made-up addresses, far enough apart for the sizes below."""
+    return ctypes.c_void_p(base * step)
+
+
+def test_overlapping_buffers_are_refused(lib):
+    g = ctypes.byref(gate())
+    T, H, E = 64, 1024, 256
+    x, w, bias, bal, lo, i, tw, ws, r, s, y, q, qs = (_at(n + 1) for n in range(13))
+
+    def inside(p, off):
+        return ctypes.c_void_p(p.value + off)
+    f = lib.dwdp_gate_topk
+    for args in ((lo, bal, lo, tw), (lo, bal, i, inside(lo, T * E * 4 - 4)), (lo, bal, i, i), (lo, bal, bal, tw),
+                 (lo, bal, inside(tw, T * 8 * 4 - 4), tw)):
+        expect(f(args[0], args[1], T, E, g, args[2], args[3], None), lib, "overlaps")
+
+    need = lib.dwdp_route_gate_workspace_bytes(T, H, E, 1)
+    assert need > 0
+    base = dict(x=x, w=w, bias=bias, bal=bal, lo=lo, i=i, tw=tw, ws=ws)
+
+    def route(**kw):
+        a = dict(base, **kw)
+        return lib.dwdp_route_gate(a["x"], a["w"], 1, a["bias"], a["bal"], T, H, E, g, a["lo"], a["i"], a["tw"], a["ws"],
+                                   need, None)
+    for kw in (dict(lo=x), dict(lo=inside(w, E * H * 2 - 4)), dict(i=lo), dict(tw=i), dict(ws=x), dict(ws=lo), dict(i=ws),
+               dict(tw=bal), dict(lo=bias), dict(x=inside(ws, need - 16))):
+        expect(route(**kw), lib, "overlaps")
+
+    nbase = dict(x=x, r=r, w=w, s=s, y=y, q=q, qs=qs)
+
+    def norm(**kw):
+        a = dict(nbase, **kw)
+        return lib.dwdp_add_rmsnorm(a["x"], a["r"], 1, a["w"], 1, 1e-6, T, H, a["s"], a["y"], a["q"], a["qs"], None)
+
+    def combine(**kw):
+        a = dict(nbase, ip=i, tw=tw, **kw)
+        return lib.dwdp_combine_add_rmsnorm(a["x"], a["ip"], a["tw"], T, 8, 1, H, 1, a["r"], a["w"], 1, 1e-6, a["s"], a["y"],
+                                            a["q"], a["qs"], None)
+    row = H * 2
+    for kw in (dict(s=inside(r, row)), dict(y=inside(r, -row)), dict(q=r), dict(q=x), dict(qs=x), dict(qs=w), dict(y=w),
+               dict(q=s), dict(y=inside(s, row)), dict(qs=inside(q, T * H - 4)), dict(w=inside(y, row))):
+        expect(norm(**kw), lib, "overlaps")
+        expect(combine(**kw), lib, "overlaps" if kw.get("q") is not x else "is an output")
+    expect(norm(s=inside(x, row)), lib, "overlaps")
+    for kw in (dict(s=inside(x, 9 * T * row - row)), dict(y=i), dict(qs=tw)):
+        expect(combine(**kw), lib, "overlaps")
+
+
 def test_gate_object():
     from split_weight_expert_amd import api
     g = api.Gate(k=8, score="sigmoid", n_groups=8, topk_groups=4, group_top=2, scale=2.5)
@@ -168,6 +217,8 @@ def test_gate_object():
         assert h == g and bytes(h._c) == bytes(g._c)
     with pytest.raises(ValueError):
         api.Gate(k=8, score="relu")
+    with pytest.raises(ValueError, match="32-bit"):
+        api.Gate(k=8, n_groups=(1 << 32) + 1)
 
 
 def test_binding_refuses_tensors_that_are_not_on_the_gpu():
@@ -185,6 +236,8 @@ def test_binding_refuses_tensors_that_are_not_on_the_gpu():
         api.combine_add_rmsnorm(x, torch.zeros(2, 2, dtype=torch.int32), tw, 0, None, None, 1e-6, sum_out=x)
     with pytest.raises(ValueError, match="2 dimensions"):
         api.gate_topk(lo[0], g, i, tw)
+    with pytest.raises(ValueError, match="columns"):       # 2^32 + 8 columns would be 8 to the library
+        api.add_rmsnorm(torch.empty(1, (1 << 32) + 8, device="meta"), None, x[0], 1e-6, y=x)
     with pytest.raises(ValueError, match="the block is for"):
         MoEBlock(256, 128, 8, 3, 0, "f32", "cpu", gate=g)
 
