@@ -39,6 +39,10 @@ __device__ __forceinline__ void store_logit(const RouterArgs& a, int slice, int6
 // 16 (l / 16) of the step; a step is 64 bytes of a row.  bf16: one v_mfma_f32_16x16x32_bf16 a step; fp32: four
 // v_mfma_f32_16x16x4_f32, each taking one of the four consecutive columns a lane holds, which is the same
 // columns on both sides.  Result element r of lane l: token 4 (l / 16) + r, expert l % 16.
+//
+// Bound by latency: one token of 7168 bf16 columns against 256 experts takes 3.9 us for 3.7 MB of weights, 64
+// tokens 7.4 us, of which an empty kernel takes 2.3; eight 64-byte steps of both operands are in flight a wave (four
+// with 16 waves, or sixteen with four, were no faster).
 constexpr int kFewWaves = 4;
 
 template <bool BF16>
@@ -121,7 +125,14 @@ __device__ __forceinline__ void wait_steps(int steps) {   // at most `steps` (<=
 // k + NS - 1 is the one step k - 1 read, so it is filled after step k's barrier, and its DMAs are issued between
 // the step's products: issued in one go they hold up the wave, and with it the products, for as long as the
 // address unit takes them.  16-byte chunk c of row r sits in slot c ^ ((r / 2) % 8) of its row, so that 16
-// consecutive rows read at one chunk spread over all banks.
+// consecutive rows read at one chunk spread over all banks (counted: no bank conflict).
+//
+// 8192 x 7168 tokens and 256 experts (128 x 256 tiles, 4 slices): 42 us, 709 TFLOP/s; it reads 125 MB from HBM, every
+// token once, and 350 MB through the DMAs, which alone take 35 us, and keeps the matrix cores busy for 27% of
+// the time.  So what bounds it is the DMAs' way from L2 to LDS, with one workgroup's barrier per step; with the DMAs
+// issued together before the products it took 54.7 us.  Not faster: larger tiles for fewer bytes (256 x 128, tokens
+// straight into registers: 74.6 us with the gate, against 58.9), smaller ones for two workgroups per compute unit (15%
+// slower), four waves of larger tiles (45 and 47 us), 16 waves (the same).
 template <int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a) {
     constexpr int NW = WM * WN, ROWB = 128, STAGE = (BM + BN) * ROWB, P = NS - 1;
