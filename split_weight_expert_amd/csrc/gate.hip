@@ -205,12 +205,15 @@ __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
 // Error bounds (u = 2^-24).  exp2 and rcp have errors of 2 u, products and sums 1 u.
 //   sigmoid: s = 1 / (1 + e), e = exp2(-l log2e): the exponent's error enters e relative by 1.5 |l| u, so s is
 //     off by at most s (1 - s) (1.5 |l| + 2) u + 3 s u <= 3.9 u, since s (1 - s) |l| <= 0.23.
-//   softmax: f = exp2((l - m) log2e) / S with S >= 1: the numerator is off by at most 3 u, S by 42 u relative
-//     (the mean of |l - m| under the softmax is at most ln 1024), so s by at most 51 u / S, as s <= 1 / S.
+//   softmax: n = exp2((l - m) log2e) with x = |l - m|: off by n (2.23 x + 2) u <= 2.1 u, as n = e^-x.  S, the sum of n, is off
+//     relative by the mean of that under the softmax, (2.23 ln E + 2) u since the mean of x is at most ln E, and
+//     by u for each level of the pairwise sum, log2 E.  With reciprocal and product s = n / S is off by at most
+//     (2.1 + 2.23 ln E + 2 + log2 E + 3) u / S: 30 u / S up to 512 experts, 33 u / S up to 1024.
 //   the bias' addition adds u |c|.
 // Two keys: twice that.  kTol* are those sums rounded up to powers of two.
 constexpr float kTolSigmoid = 0x1p-21f;       // >= 2 * 3.9 u
-constexpr float kTolSoftmax = 0x1p-17f;       // >= 2 * 51 u, times 1 / S
+constexpr float kTolSoftmax = 0x1p-18f;       // >= 2 * 30 u, times 1 / S
+constexpr float kTolSoftmax1024 = 0x1p-17f;   // >= 2 * 33 u, times 1 / S
 constexpr float kTolChoice = 0x1p-22f;        // >= 2 u, times the key
 
 constexpr uint32_t kKeyMask = 1023;           // expert numbers: E <= 1024
@@ -346,15 +349,31 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     auto logits_written = [&] {
         if constexpr (SLICED) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
     };
-    // The softmax's denominator and an expert's choice in fp64, for close calls.  m: the largest logit.
-    auto softmax_total = [&](int64_t t, float m) {
-        double s = 0.0;
+    // The softmax's denominator and an expert's choice in fp64, for close calls.  m: the largest logit.  The whole
+    // wave works on each token that has a lane in `need`, four experts a lane at a time: on the token's own 16 lanes the
+    // 16 exponentials of 256 experts, one by one, took 3 us longer (4096 tokens, a softmax with a bias).
+    auto softmax_total = [&](unsigned long long need, int64_t t0, float m) {
+        double total = 1.0;
+        for (int i = 0; i < TPW; ++i) {
+            if ((need & (kToken << (i * L))) == 0) continue;
+            const float* row = a.logits + min(t0 + i, a.T - 1) * a.E;
+            const float mi = __shfl(m, i * L);
+            double s = 0.0;
 #pragma unroll 1
-        for (int i = 0; i < PL; ++i) {                // rolled: rare, and registers are dear
-            const float x = i < count ? a.logits[t * a.E + base + i] : f_neg_inf();
-            if (x > f_neg_inf()) s += x == m ? 1.0 : exp((double)x - (double)m);
+            for (int e0 = lane; e0 - lane < a.E; e0 += 256) {
+                float x[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) x[u] = e0 + 64 * u < a.E ? row[e0 + 64 * u] : f_neg_inf();
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const double e = exp(x[u] == mi ? 0.0 : (double)x[u] - (double)mi);
+                    s += x[u] > f_neg_inf() ? e : 0.0;
+                }
+            }
+            s = over_token<64>(s, AddD());
+            if (tok == i) total = s;
         }
-        return over_token<L>(s, AddD());
+        return total;
     };
     auto choice64 = [&](int64_t t, int e, float m, double total) {
         const float x = a.logits[t * a.E + e];
@@ -417,16 +436,20 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         float c[PL];                                  // choices; without a bias the logits, or scores for the groups
         if (!a.sigmoid && (need_scores || !a.renorm)) {
             m = over_token<L>(m, MaxF());
-            sum = 0.0f;
+            float part[PL];                           // summed pairwise: each addition's error counts log2 PL times
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
                 c[i] = l[i] == m ? 1.0f : __builtin_amdgcn_exp2f((l[i] - m) * kLog2e);
                 c[i] = l[i] > f_neg_inf() ? c[i] : 0.0f;
-                sum += c[i];
+                part[i] = c[i];
             }
-            sum = over_token<L>(sum, AddF());
+#pragma unroll
+            for (int d = PL / 2; d >= 1; d /= 2)
+#pragma unroll
+                for (int i = 0; i < d; ++i) part[i] += part[i + d];
+            sum = over_token<L>(part[0], AddF());
             const float inv = __builtin_amdgcn_rcpf(sum);
-            tol = kTolSoftmax * inv;
+            tol = (L * PL <= 512 ? kTolSoftmax : kTolSoftmax1024) * inv;
 #pragma unroll
             for (int i = 0; i < PL; ++i) c[i] *= inv;
         } else if (need_scores) {
@@ -495,16 +518,18 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
 #pragma unroll
                 for (int i = 0; i < PL; ++i)
                     third |= c[i] > f_neg_inf() && base + i != e1 && base + i != e2 && !((pairs ? b2 : b1) - c[i] >= margin);
-                const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
+                const double total = a.sigmoid ? 1.0 : softmax_total(who, t0, m);
                 const double c1 = gone(k1) ? -__builtin_huge_val() : choice64(t, e1, m, total);
                 const double c2 = gone(k2) ? -__builtin_huge_val() : choice64(t, e2, m, total);
                 const double v = gone(k2) ? c1 : pairs ? c1 + c2 : fmax(c1, c2);
-                before = 0;
+                int before64 = 0;
                 for (int h = 0; h < a.groups; ++h) {
                     const double o = __shfl(v, h << a.lane_shift, L);
-                    before += o > v || (o == v && h < g);
+                    before64 += o > v || (o == v && h < g);
                 }
-                unsure = (who & (kToken << (lane & ~(L - 1)))) != 0 && third && !(fabsf(value - border) >= 2.0f * margin);
+                const bool again = (who & (kToken << (lane & ~(L - 1)))) != 0;   // this token; no other has a total
+                before = again ? before64 : before;
+                unsure = again && third && !(fabsf(value - border) >= 2.0f * margin);
             }
             kept = before < a.kept && g < a.groups;
         }
@@ -529,9 +554,10 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         bool has = q < a.k && !gone(picked);
         int my_i = gone(picked) ? 0 : key_expert(picked);
         logits_written();
-        if (__ballot(close) != 0) {
+        const unsigned long long closes = __ballot(close);
+        if (closes != 0) {
             // prev is the best expert that is no candidate
-            const double total = a.sigmoid ? 1.0 : softmax_total(t, m);
+            const double total = a.sigmoid ? 1.0 : softmax_total(closes, t0, m);
             const bool cand = q <= a.k && !gone(picked);
             const double c = cand ? choice64(t, my_i, m, total) : -__builtin_huge_val();
             int rank = 0;
@@ -632,7 +658,7 @@ bool launch_lanes(GateArgs& a, hipStream_t st) {
     const size_t lds = a.groups > 1 ? 4 * (size_t)(a.E + a.groups) * sizeof(double) : 0;   // for gate_row_exact
     constexpr int64_t kTokens = 4 * (64 / L);         // per workgroup
     // a launch takes up to kMaxRowGrid workgroups (a loop over tokens in the kernel would keep what is the same
-    // for all of them in registers: 200 instead of 131)
+    // for all of them in registers: 200 against 131 when tried)
     for (a.first = 0; a.first < a.T; a.first += kMaxRowGrid * kTokens) {
         const dim3 grid((unsigned)std::min<int64_t>((a.T - a.first + kTokens - 1) / kTokens, kMaxRowGrid));
         if (a.part != nullptr) hipLaunchKernelGGL((gate_lanes_kernel<L, PL, true>), grid, dim3(256), lds, st, a);
@@ -657,14 +683,15 @@ bool lanes_hold(const GateArgs& a) {
 }
 
 int launch_gate(GateArgs a, hipStream_t st) {
-    // Up to 2048 tokens the chip has room for a wave each, and 64 lanes are done sooner (64 tokens x 256 experts,
-    // k = 8, sigmoid with a bias and groups: 5.3 against 6.8 us); beyond, four tokens to a wave spend fewer
-    // instructions on each (4096 tokens: 7.1 against 7.9 us; 16K: 13.8 against 22.6).
-    const bool few = a.T <= 2048;
     if (lanes_hold(a)) {
-        // the narrowest layout that holds it
-        (!few && (launch_lanes<16, 4>(a, st) || launch_lanes<16, 8>(a, st) || launch_lanes<16, 16>(a, st))) ||
-            launch_lanes<64, 4>(a, st) || launch_lanes<64, 8>(a, st) || launch_lanes<64, 16>(a, st);
+        // The narrowest layout that holds it: four tokens to a wave spend fewer instructions on each, 64 lanes on one
+        // are done sooner as long as the chip has room for the waves.  16 against 64 lanes, us:
+        //   4 experts a lane (64 experts, k = 8): 1 token 3.0 and 3.3, 1777 tokens 3.5 and 4.3
+        //   8 (128, sigmoid with a bias):         64 tokens 4.5 and 4.3, 1777 4.7 and 4.8, 4096 5.0 and 6.0
+        //   16 (256, the same and 4 of 8 groups): 64 tokens 6.8 and 5.4, 2048 7.0 and 6.0, 3500 7.4 and 8.1
+        launch_lanes<16, 4>(a, st) || (a.T > 1024 && launch_lanes<16, 8>(a, st)) ||
+            (a.T > 2048 && launch_lanes<16, 16>(a, st)) || launch_lanes<64, 4>(a, st) || launch_lanes<64, 8>(a, st) ||
+            launch_lanes<64, 16>(a, st);
     } else if (a.E <= 256) {
         launch_exact<4>(a, st);
     } else if (a.E <= 512) {
