@@ -66,8 +66,8 @@ typedef struct {
  *   ws: dwdp_route_gate_workspace_bytes(...) bytes of device scratch, 16-byte aligned (NULL if 0); its
  *   contents need no preparation and mean nothing after the call.  Calls that may run at the same time
  *   need a workspace each.
- *   No output, nor ws, may overlap another buffer.  T is limited by one launch of the product (bf16: 10^9
- *   tokens and more; f32: about 8 million tokens of 256 experts); larger ones are refused. */
+ *   No output, nor ws, may overlap another buffer.  T is limited by one launch of the product: more than 10^8
+ *   tokens of 256 experts (f32 with H % 32 != 0: 8 * 10^6); larger batches are refused. */
 int dwdp_route_gate(const void* x, const void* w_router, int in_dtype, const float* bias,
                     const float* balance_bias, int64_t T, int H, int E, const dwdp_gate* gate,
                     float* logits_out, int32_t* topk_idx, float* topk_w, void* ws, size_t ws_bytes,

@@ -2,10 +2,10 @@
 // every batch fills the chip.  With one slice the logits are written (bias added); with more, each slice's
 // partial sums go to part[slice][T][E] and the gate's kernel adds them, in slice order, as it reads them.
 //
-//   few tokens   router_few_kernel: 16 x 16 tiles, operands straight from global memory into the matrix
-//                instruction; bound by latency, and by the weights' bytes
-//   many tokens  router_tile_kernel: BM x BN tiles, operands by DMA into an LDS ring; bound by the tokens'
-//                bytes and the matrix cores
+//   small products  router_few_kernel: 16 x 16 tiles, operands straight from global memory into the matrix
+//                   instruction; bound by latency, and by the weights' bytes
+//   the others      router_tile_kernel: BM x BN tiles, operands by DMA into an LDS ring; bound by the DMAs
+//                   (bf16) or by the matrix cores (fp32)
 #include <algorithm>
 
 #include "common.h"
@@ -40,10 +40,10 @@ __device__ __forceinline__ void store_logit(const RouterArgs& a, int slice, int6
 // v_mfma_f32_16x16x4_f32, each taking one of the four consecutive columns a lane holds, which is the same
 // columns on both sides.  Result element r of lane l: token 4 (l / 16) + r, expert l % 16.
 //
-// Bound by latency: one token of 7168 bf16 columns against 256 experts takes 3.9 us for 3.7 MB of weights, 64
-// tokens 7.4 us, of which an empty kernel takes 2.3; eight 64-byte steps of both operands are in flight a wave (four
-// with 16 waves, or sixteen with four, were no faster).
-constexpr int kFewWaves = 4;
+// Bound by latency: one token of 7168 bf16 columns against 256 experts takes 4.9 us for 3.7 MB of weights, 64
+// tokens 6.8 us, of which an empty kernel takes 2.3; eight 64-byte steps of both operands are in flight a wave (four
+// were as fast).  Eight waves share a tile's steps: with four, 64 tokens took 0.8 us longer, 16 were no faster.
+constexpr int kFewWaves = 8;
 
 template <bool BF16>
 __global__ __launch_bounds__(kFewWaves * 64) void router_few_kernel(RouterArgs a) {
@@ -120,7 +120,8 @@ __device__ __forceinline__ void wait_steps(int steps) {   // at most `steps` (<=
     else wait_steps<PER, MOST - 1>(steps);
 }
 
-// One BM x BN tile of one slice, bf16.  WM x WN waves; a K step is 64 columns, 128 bytes of a row, moved into LDS
+// One BM x BN tile of one slice.  WM x WN waves; a K step is 128 bytes of a row (64 bf16 columns, or 32 fp32 ones, of which
+// a matrix instruction takes one of the four consecutive that a lane holds, the same on both sides), moved into LDS
 // by 1 KB DMA instructions of 8 rows each, into a ring of NS slots with NS - 1 steps in flight.  The slot of step
 // k + NS - 1 is the one step k - 1 read, so it is filled after step k's barrier, and its DMAs are issued between
 // the step's products: issued in one go they hold up the wave, and with it the products, for as long as the
@@ -132,8 +133,9 @@ __device__ __forceinline__ void wait_steps(int steps) {   // at most `steps` (<=
 // the time.  So what bounds it is the DMAs' way from L2 to LDS, with one workgroup's barrier per step; with the DMAs
 // issued together before the products it took 54.7 us.  Not faster: larger tiles for fewer bytes (256 x 128, tokens
 // straight into registers: 74.6 us with the gate, against 58.9), smaller ones for two workgroups per compute unit (15%
-// slower), four waves of larger tiles (45 and 47 us), 16 waves (the same).
-template <int BM, int BN, int WM, int WN, int NS>
+// slower), four waves of larger tiles (45 and 47 us), 16 waves (the same).  fp32: 8192 x 7168 and 256 experts, 64 x 64 tiles,
+// 260 us, 116 TFLOP/s, three quarters of the fp32 matrix rate of 157.
+template <bool BF16, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a) {
     constexpr int NW = WM * WN, ROWB = 128, STAGE = (BM + BN) * ROWB, P = NS - 1;
     constexpr int TM = BM / WM, TN = BN / WN, MI = TM / 32, NJ = TN / 32;
@@ -152,7 +154,8 @@ __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a)
     const int m = (int)(lin % a.m_tiles), n = (int)(lin / a.m_tiles % a.n_tiles), slice = (int)(lin / a.m_tiles / a.n_tiles);
     const int64_t m0 = (int64_t)m * BM;
     const int n0 = n * BN;
-    const int steps = a.H / 64;
+    const int64_t row_bytes = (int64_t)a.H * (BF16 ? 2 : 4);
+    const int steps = (int)(row_bytes / ROWB);
     const int kb = (int)((int64_t)slice * steps / a.slices), KT = (int)((int64_t)(slice + 1) * steps / a.slices) - kb;
 
     const uint8_t* g[PER];
@@ -160,14 +163,14 @@ __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a)
     for (int i = 0; i < PER; ++i) {
         const int r = (wave * PER + i) * 8 + lane / 8;    // row of the stage: BM token rows, then BN expert rows
         const int c = (lane & 7) ^ ((r >> 1) & 7);
-        g[i] = (r < BM ? a.x + min(m0 + r, a.T - 1) * a.H * 2 : a.w + (int64_t)min(n0 + r - BM, a.E - 1) * a.H * 2) +
+        g[i] = (r < BM ? a.x + min(m0 + r, a.T - 1) * row_bytes : a.w + min(n0 + r - BM, a.E - 1) * row_bytes) +
                (int64_t)kb * ROWB + c * 16;
     }
     auto issue = [&](int kt, int i) {
         dma16(g[i] + (int64_t)kt * ROWB, ring + kt % NS * STAGE + (wave * PER + i) * 1024);
     };
     auto frag = [&](const uint8_t* s, int row, int chunk) {
-        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const f32x4*>(s + row * ROWB + ((chunk ^ ((row >> 1) & 7)) << 4)));
+        return *reinterpret_cast<const f32x4*>(s + row * ROWB + ((chunk ^ ((row >> 1) & 7)) << 4));
     };
     f32x16 acc[MI][NJ];
 #pragma unroll
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a)
         const uint8_t* A = ring + kt % NS * STAGE;
         const uint8_t* B = A + BM * ROWB;
         const bool more = kt + P < KT;
-        bf16x8 af[4][MI], bf[4][NJ];
+        f32x4 af[4][MI], bf[4][NJ];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
 #pragma unroll
@@ -199,8 +202,17 @@ __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a)
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(af[s][i], bf[s][j], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < NJ; ++j) {
+                    if constexpr (BF16) {
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, af[s][i]),
+                                                                            __builtin_bit_cast(bf16x8, bf[s][j]),
+                                                                            acc[i][j], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(af[s][i][c], bf[s][j][c], acc[i][j], 0, 0, 0);
+                    }
+                }
             __builtin_amdgcn_sched_barrier(0);
             if (more)
 #pragma unroll
@@ -220,30 +232,37 @@ __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a)
                             acc[i][j][r]);
 }
 
-template <int BM, int BN, int WM, int WN, int NS>
+template <bool BF16, int BM, int BN, int WM, int WN, int NS>
 void launch_tile(const RouterArgs& a, hipStream_t st) {
     const int64_t tiles = (int64_t)a.m_tiles * a.n_tiles * a.slices;
     const unsigned grid = (unsigned)((tiles + kNumXcd - 1) / kNumXcd * kNumXcd);
-    hipLaunchKernelGGL((router_tile_kernel<BM, BN, WM, WN, NS>), dim3(grid), dim3(WM * WN * 64), 0, st, a);
+    hipLaunchKernelGGL((router_tile_kernel<BF16, BM, BN, WM, WN, NS>), dim3(grid), dim3(WM * WN * 64), 0, st, a);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Measured on 7168-wide bf16 tokens and 256 experts, product and gate together, other inputs in between:
-//   tokens     64: 16 x 16 tiles 14.2 us, 64 x 64 tiles 15.2          128: 16.7 and 15.5
-//   tokens   1024: 64 x 64 tiles 19.2 us, 64 x 256 21.7              2048: 25.4 and 25.8    4096: 45.6 and 36.6
-//   tokens   4096: 64 x 256 tiles 36.6 us, 128 x 256 40.1            8192: 64.5 and 58.5
-// Slices: as many as give the chip's 256 compute units a tile each (two of the 64 x 64 ones), but no more than 8,
-// since the gate reads what every slice writes (one token: 8 slices 10.7 us, 16 12.4), of 4 K steps at least.
+// Measured, product and gate together in a graph, other inputs in between (us):
+//   16 x 16 tiles or 64 x 64: each 16 x 16 tile reads 32 rows, so it is the bytes of a row times the tiles that decide.
+//     bf16  0.9 MB (64 tokens x 7168, 256 experts) 12.6 and 14.3, 1.1 MB (80 tokens) 13.6 and 14.9, 1.4 MB (96) 15.5 and
+//           14.6, 1.8 MB (1777 x 1984, 60 experts) 15.0 and 12.6
+//     fp32  0.9 MB (200 x 1024, 256 experts) 11.9 and 13.6, 1.8 MB (64 x 7168) 17.0 and 29.1, 4.2 MB (512 x 1024, 512
+//           experts) 26.3 and 17.8, 235 MB (8192 x 7168, 256 experts) 883 and 279
+//   wider tiles, bf16, 7168 columns, 256 experts: 1024 tokens 64 x 64 19.2, 64 x 256 21.7; 2048: 25.4 and 25.8; 4096: 45.6 and
+//     36.6; 4096: 64 x 256 36.6, 128 x 256 40.1; 8192: 64.5 and 58.5.  fp32 is bound by its matrix instructions on any tile.
+// Slices: as many as give the chip's 256 compute units a tile each (two of the 64 x 64 ones), but few enough that the
+// gate's reading of them costs less than they save: for 16 x 16 tiles at most 4 (8: 16 tokens x 5376, 452 experts
+// 16.9 against 14.8), of 16 K steps at least; else 8, of 8 K steps at least (4: 567 x 2176, 226 experts 14.9 against 13.5).
 RouterPlan plan_router(int64_t T, int H, int E, int dtype) {
     RouterPlan p{};
-    const int64_t t64 = ceil_div(T, 64);
+    const bool bf16 = dtype == DWDP_BF16;
+    const int64_t t64 = ceil_div(T, 64), row_bytes = (int64_t)H * (bf16 ? 2 : 4);
     int64_t want = 256;
-    if (dtype != DWDP_BF16 || T <= 64) {
+    // fp32 rows need not be a multiple of the wider tiles' 128-byte K step
+    if (ceil_div(T, 16) * ceil_div(E, 16) * row_bytes <= (bf16 ? 5 << 18 : 2 << 20) || row_bytes % 128 != 0) {
         p.bm = p.bn = 16;
-    } else if (E <= 64 || t64 * ceil_div(E, 64) <= 128) {
+    } else if (!bf16 || E <= 64 || t64 * ceil_div(E, 64) <= 128) {
         p.bm = p.bn = 64;
         want = 512;
     } else if (E <= 128) {
@@ -254,8 +273,8 @@ RouterPlan plan_router(int64_t T, int H, int E, int dtype) {
         p.bn = 256;
     }
     const int64_t tiles = ceil_div(T, p.bm) * ceil_div(E, p.bn);
-    const int64_t steps = (int64_t)H * (dtype == DWDP_BF16 ? 2 : 4) / (p.bm == 16 ? 64 : 128);
-    p.slices = (int)std::max<int64_t>(1, std::min({want / tiles, steps / 4, (int64_t)8}));
+    const int64_t most = p.bm == 16 ? std::min<int64_t>(4, row_bytes / 64 / 16) : std::min<int64_t>(8, row_bytes / 128 / 8);
+    p.slices = (int)std::max<int64_t>(1, std::min(want / tiles, most));
     return p;
 }
 
@@ -283,13 +302,15 @@ int router_split(const void* x, const void* w, int dtype, const float* bias, int
         if (dtype == DWDP_BF16) hipLaunchKernelGGL(router_few_kernel<true>, grid, block, 0, st, a);
         else hipLaunchKernelGGL(router_few_kernel<false>, grid, block, 0, st, a);
     } else if (p.bm == 128) {
-        launch_tile<128, 256, 2, 4, 3>(a, st);
+        launch_tile<true, 128, 256, 2, 4, 3>(a, st);
     } else if (p.bn == 256) {
-        launch_tile<64, 256, 2, 4, 4>(a, st);
+        launch_tile<true, 64, 256, 2, 4, 4>(a, st);
     } else if (p.bn == 128) {
-        launch_tile<64, 128, 2, 2, 3>(a, st);
+        launch_tile<true, 64, 128, 2, 2, 3>(a, st);
+    } else if (dtype == DWDP_BF16) {
+        launch_tile<true, 64, 64, 2, 2, 4>(a, st);
     } else {
-        launch_tile<64, 64, 2, 2, 4>(a, st);
+        launch_tile<false, 64, 64, 2, 2, 4>(a, st);
     }
     DWDP_LAUNCHED();
     return DWDP_OK;

@@ -253,6 +253,33 @@ def test_route_gate_matches_the_oracle(T, H, E, k, groups, kept, dt):
         check_gate(lo[:T], gate, bb, idx[:T], w[:T])
 
 
+@pytest.mark.parametrize("T,H,E,k,groups,kept,dt", [
+    (513, 1056, 256, 8, 8, 4, "f32"), (1030, 2080, 72, 6, 1, 1, "f32"), (700, 1040, 512, 8, 4, 2, "f32"), (70, 7168, 300, 7, 5, 2, "f32"),
+    (9000, 64, 320, 4, 1, 1, "f32"), (2500, 416, 1000, 12, 8, 3, "f32"), (3000, 1024, 33, 4, 1, 1, "f32"), (80, 7168, 256, 8, 8, 4, "bf16"),
+    (96, 7168, 256, 8, 8, 4, "bf16"), (40, 5376, 452, 12, 2, 2, "bf16"), (1000, 512, 128, 4, 1, 1, "bf16"), (2000, 64, 1000, 8, 1, 1, "bf16"),
+    (3, 4096, 1024, 8, 16, 4, "bf16"), (1681, 2048, 168, 9, 8, 1, "bf16"),
+])
+def test_route_gate_of_every_tile_and_slice(T, H, E, k, groups, kept, dt):
+    """Small and large products of both types, in one slice and in several, with ragged tiles and K steps."""
+    test_route_gate_matches_the_oracle(T, H, E, k, groups, kept, dt)
+
+
+@pytest.mark.parametrize("T,H,E", [(7, 1008, 68), (200, 1024, 200), (600, 1056, 256), (300, 4096, 200), (1100, 1040, 100)])
+def test_route_gate_random_fp32_values(T, H, E):
+    """A logit's error is that of H rounded products and an fp32 sum of them in any order."""
+    from split_weight_expert_amd import api
+    g = gen(T)
+    x = torch.randn(T, H, generator=g, device=DEV)
+    wr = torch.randn(E, H, generator=g, device=DEV) * H ** -0.5
+    gate = make_gate(6, "sigmoid")
+    idx, w, lo = gate_outputs(T, 6, E)
+    api.route_gate(x, wr, gate, lo[:T], idx[:T], w[:T], route_ws(T, H, E, x)[1])
+    xd, wd = x.double(), wr.double()
+    bound = (xd.abs() @ wd.abs().t().contiguous()) * (H + 1) * U32 * 1.01      # 1.01: the products of errors
+    assert ((lo[:T].double() - xd @ wd.t().contiguous()).abs() <= bound).all()
+    check_gate(lo[:T], gate, None, idx[:T], w[:T])
+
+
 def test_route_gate_random_values():
     """Ordinary bf16 values: a logit's error is that of an fp32 sum of H exact products in any order."""
     from split_weight_expert_amd import api
