@@ -134,7 +134,7 @@ __device__ __forceinline__ void wait_steps(int steps) {   // at most `steps` (<=
 // issued together before the products it took 54.7 us.  Not faster: larger tiles for fewer bytes (256 x 128, tokens
 // straight into registers: 74.6 us with the gate, against 58.9), smaller ones for two workgroups per compute unit (15%
 // slower), four waves of larger tiles (45 and 47 us), 16 waves (the same).  fp32: 8192 x 7168 and 256 experts, 64 x 64 tiles,
-// 260 us, 116 TFLOP/s, three quarters of the fp32 matrix rate of 157.
+// about 250 us, 120 TFLOP/s, three quarters of the fp32 matrix rate of 157.
 template <bool BF16, int BM, int BN, int WM, int WN, int NS>
 __global__ __launch_bounds__(WM * WN * 64) void router_tile_kernel(RouterArgs a) {
     constexpr int NW = WM * WN, ROWB = 128, STAGE = (BM + BN) * ROWB, P = NS - 1;
