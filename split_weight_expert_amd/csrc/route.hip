@@ -206,26 +206,6 @@ __global__ __launch_bounds__(256) void topk_kernel(const float* __restrict__ log
 }
 
 }  // namespace
-
-// The router product of checked arguments (T >= 1), whichever kernel the batch takes.
-int router_logits(const void* x, const void* w_router, int in_dtype, const float* bias, int64_t T, int H, int E,
-                  float* logits, hipStream_t st) {
-    if (DWDP_ROUTER_SPLITK_TILE == 16 && in_dtype == DWDP_BF16 && T <= kSplitMaxT) {
-        hipLaunchKernelGGL(router_splitk16_kernel, dim3((unsigned)((T + 15) / 16), (unsigned)((E + 15) / 16)),
-                           dim3(kSplit16Waves * 64), 0, st, static_cast<const uint16_t*>(x),
-                           static_cast<const uint16_t*>(w_router), bias, (int)T, H, E, logits);
-        DWDP_LAUNCHED();
-    } else if (in_dtype == DWDP_BF16 && T <= kSplitMaxT && H % (kSplitWaves * 16) == 0) {
-        hipLaunchKernelGGL(router_splitk_kernel, dim3((unsigned)((T + 31) / 32), (unsigned)((E + 31) / 32)),
-                           dim3(kSplitWaves * 64), 0, st, static_cast<const uint16_t*>(x),
-                           static_cast<const uint16_t*>(w_router), bias, (int)T, H, E, logits);
-        DWDP_LAUNCHED();
-    } else {
-        return router_gemm(x, w_router, in_dtype, bias, T, H, E, logits, st);
-    }
-    return DWDP_OK;
-}
-
 }  // namespace dwdp
 
 using namespace dwdp;
@@ -244,8 +224,20 @@ extern "C" int dwdp_route_topk(const void* x, const void* w_router, int in_dtype
     DWDP_REQUIRE(x && w_router && logits_out && topk_idx && topk_w, "null pointer argument");
     DWDP_REQUIRE(aligned16(x) && aligned16(w_router), "x and w_router must be 16-byte aligned");
     hipStream_t st = as_stream(stream);
-    int rc = router_logits(x, w_router, in_dtype, bias, T, H, E, logits_out, st);
-    if (rc != DWDP_OK) return rc;
+    if (DWDP_ROUTER_SPLITK_TILE == 16 && in_dtype == DWDP_BF16 && T <= kSplitMaxT) {
+        hipLaunchKernelGGL(router_splitk16_kernel, dim3((unsigned)((T + 15) / 16), (unsigned)((E + 15) / 16)),
+                           dim3(kSplit16Waves * 64), 0, st, static_cast<const uint16_t*>(x),
+                           static_cast<const uint16_t*>(w_router), bias, (int)T, H, E, logits_out);
+        DWDP_LAUNCHED();
+    } else if (in_dtype == DWDP_BF16 && T <= kSplitMaxT && H % (kSplitWaves * 16) == 0) {
+        hipLaunchKernelGGL(router_splitk_kernel, dim3((unsigned)((T + 31) / 32), (unsigned)((E + 31) / 32)),
+                           dim3(kSplitWaves * 64), 0, st, static_cast<const uint16_t*>(x),
+                           static_cast<const uint16_t*>(w_router), bias, (int)T, H, E, logits_out);
+        DWDP_LAUNCHED();
+    } else {
+        int rc = router_gemm(x, w_router, in_dtype, bias, T, H, E, logits_out, st);
+        if (rc != DWDP_OK) return rc;
+    }
     const dim3 tgrid((unsigned)std::min<int64_t>((T + 3) / 4, kMaxRowGrid));
     if (E <= 64) hipLaunchKernelGGL(topk_kernel<1>, tgrid, dim3(256), 0, st, logits_out, T, E, k, topk_idx, topk_w);
     else if (E <= 128) hipLaunchKernelGGL(topk_kernel<2>, tgrid, dim3(256), 0, st, logits_out, T, E, k, topk_idx, topk_w);
