@@ -235,12 +235,12 @@ class MoEBlock:
     def _norm_outputs(self, b: BlockBuffers):
         if b.x_norm is None:
             b.x_norm = torch.empty_like(b.y)
-        b.normed = True
         return dict(y=b.x_norm, q=b.x_q, q_scale=b.x_q_scale)
 
     def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None):
         """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given)."""
         api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b))
+        b.normed = True
 
     def forward_normed(self, h, w_router, bias, table, next_weight=None, eps: float = 1e-6, stream=None, out=None,
                        balance_bias=None) -> BlockBuffers:

@@ -89,6 +89,10 @@ def test_a_forward_in_between_takes_the_normed_input():
     blk = MoEBlock(cfg.H, cfg.I, cfg.E, cfg.k, cfg.shared, cfg.dtype, DEV, gate=make_gate(cfg))
     w = torch.ones(cfg.H, dtype=x.dtype, device=DEV)
     bb = blk.buffers(cfg.T)
+    with pytest.raises(ValueError, match="shape"):
+        blk.norm(x[1:], w, 1e-6, bb)
+    with pytest.raises(ValueError, match="no normed input"):           # a refused norm is none
+        blk.forward_normed(x, wr, b, table)
     blk.norm(x, w, 1e-6, bb)
     y0 = blk.forward_normed(x, wr, b, table, out=torch.empty_like(x)).x_norm.clone()
     first = bb.y_perm.clone()
