@@ -308,11 +308,13 @@ struct MaxKey {
 
 // Bound by instruction issue: 16K tokens x 256 experts (sigmoid, bias, 4 of 8 groups, k = 8) are 18 MB, 3.6 us of
 // memory traffic, and 1410 vector instructions for each four tokens, 9.4 us if every SIMD issued one every four
-// cycles without a pause; 13.8 us measured in a graph.  Two fifths of them are the top-k's ten rounds.
-// Keeping the logits in LDS instead of reading the chosen ones again was slower (15.9 us).
+// cycles without a pause; measured in a graph 13.8 us with the logits in the last-level cache, 15.6 with other inputs in
+// between.  Two fifths of the instructions are the top-k's ten rounds.  Not faster: keeping the logits in LDS instead
+// of reading the chosen ones again (15.9 against 13.8 us), or taking them from the lanes that hold them (0.2 us more
+// at every size).
 //
 // SLICED: the logits come as a router product's partial sums, and are written on the way; lanes that repeat the last
-// token write the same values.  4 slices of 8192 x 256 (34 MB): 18 us, against 10.4 us from logits.
+// token write the same values.  4 slices of 8192 x 256 (34 MB): 17 us, against 10 us from logits.
 template <int L, int PL, bool SLICED>
 __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     constexpr int TPW = 64 / L;                       // tokens per wave

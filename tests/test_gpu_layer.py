@@ -258,6 +258,7 @@ def test_route_gate_matches_the_oracle(T, H, E, k, groups, kept, dt):
     (9000, 64, 320, 4, 1, 1, "f32"), (2500, 416, 1000, 12, 8, 3, "f32"), (3000, 1024, 33, 4, 1, 1, "f32"), (80, 7168, 256, 8, 8, 4, "bf16"),
     (96, 7168, 256, 8, 8, 4, "bf16"), (40, 5376, 452, 12, 2, 2, "bf16"), (1000, 512, 128, 4, 1, 1, "bf16"), (2000, 64, 1000, 8, 1, 1, "bf16"),
     (3, 4096, 1024, 8, 16, 4, "bf16"), (1681, 2048, 168, 9, 8, 1, "bf16"),
+    (9000, 32, 1000, 8, 1, 1, "f32"), (9000, 64, 1000, 8, 1, 1, "bf16"), (17000, 64, 300, 8, 1, 1, "bf16"), (12000, 64, 128, 4, 1, 1, "bf16"),
 ])
 def test_route_gate_of_every_tile_and_slice(T, H, E, k, groups, kept, dt):
     """Small and large products of both types, in one slice and in several, with ragged tiles and K steps."""
