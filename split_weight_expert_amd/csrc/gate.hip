@@ -293,6 +293,23 @@ __device__ __forceinline__ V over_token(V v, Op op) {
     if constexpr (L == 64) v = with_partner<32>(with_partner<16>(v, op), op);
     return v;
 }
+// Batcher's odd-even merge sort of 16 numbers as its comparators, the larger one to place a.
+struct Net16 {
+    int n = 0;
+    int a[63] = {}, b[63] = {};
+    constexpr Net16() {
+        for (int p = 1; p < 16; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < 16; j += 2 * k)
+                    for (int i = 0; i < k; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                            a[n] = i + j;
+                            b[n++] = i + j + k;
+                        }
+    }
+};
+constexpr Net16 kNet16;
+
 struct MaxF {
     __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
 };
@@ -307,15 +324,17 @@ struct MaxKey {
 };
 
 // Bound by instruction issue: 16K tokens x 256 experts (sigmoid, bias, 4 of 8 groups, k = 8) are 18 MB, 3.6 us of
-// memory traffic, and 1410 vector instructions for each four tokens, 9.4 us if every SIMD issued one every four
-// cycles without a pause; measured in a graph 13.8 us with the logits in the last-level cache, 15.6 with other inputs in
-// between.  Two fifths of the instructions are the top-k's ten rounds.  Not faster: keeping the logits in LDS instead
-// of reading the chosen ones again (15.9 against 13.8 us), or taking them from the lanes that hold them (0.2 us more
-// at every size).
+// memory traffic, and 1200 vector instructions for each four tokens, 8.0 us if every SIMD issued one every four
+// cycles without a pause; 14.9 us measured in a graph, other inputs in between, of which a launch takes 2.3.  Not
+// faster: keeping the logits in LDS instead of reading the chosen ones again (2 us more), or taking them from the
+// lanes that hold them (0.2 us more at every size).
+//
+// SORTED: a lane's 16 keys are sorted once (126 maxima and minima), and a round takes the lane's first and moves up the
+// others, as far as later rounds can look, in place of 15 maxima and 16 comparisons with their selections.
 //
 // SLICED: the logits come as a router product's partial sums, and are written on the way; lanes that repeat the last
 // token write the same values.  4 slices of 8192 x 256 (34 MB): 17 us, against 10 us from logits.
-template <int L, int PL, bool SLICED>
+template <int L, int PL, bool SLICED, bool SORTED>
 __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     constexpr int TPW = 64 / L;                       // tokens per wave
     constexpr int XPL = L * PL <= 256 ? 4 : PL;       // experts per lane of gate_row_exact (64 lanes)
@@ -538,17 +557,38 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
         double key[PL];
 #pragma unroll
         for (int i = 0; i < PL; ++i) key[i] = make_key(!kept ? f_neg_inf() : biased ? c[i] : l[i], base + i);
+        if constexpr (SORTED) {
+#pragma unroll
+            for (int u = 0; u < kNet16.n; ++u) {
+                const double x = key[kNet16.a[u]], y = key[kNet16.b[u]];
+                key[kNet16.a[u]] = max64(x, y);
+                key[kNet16.b[u]] = min64(x, y);
+            }
+        }
         // picks 0 .. k-1, and with inexact keys two more: the next best, a candidate too, and the one behind it
         double picked = from32(kGoneHi, 0), prev = 0.0;   // picked: lane j's is pick j
         bool close = false;
         const int rounds = biased ? a.k + 2 : a.k;
         for (int j = 0; j < rounds; ++j) {
             double top = key[0];
+            if constexpr (SORTED) {
+                top = over_token<L>(top, MaxKey());
+                const bool mine = key[0] == top;
 #pragma unroll
-            for (int i = 1; i < PL; ++i) top = max64(top, key[i]);
-            top = over_token<L>(top, MaxKey());
+                for (int i = 0; i < PL; i += 4)
+                    if (i < rounds - 1 - j)           // as deep as later rounds can look
 #pragma unroll
-            for (int i = 0; i < PL; ++i) key[i] = from32(key[i] == top ? kGoneHi : hi32(key[i]), lo32(key[i]));
+                        for (int u = i; u < i + 4; ++u) {
+                            const double next = u + 1 < PL ? key[u + 1] : from32(kGoneHi, 0);
+                            key[u] = from32(mine ? hi32(next) : hi32(key[u]), mine ? lo32(next) : lo32(key[u]));
+                        }
+            } else {
+#pragma unroll
+                for (int i = 1; i < PL; ++i) top = max64(top, key[i]);
+                top = over_token<L>(top, MaxKey());
+#pragma unroll
+                for (int i = 0; i < PL; ++i) key[i] = from32(key[i] == top ? kGoneHi : hi32(key[i]), lo32(key[i]));
+            }
             if (biased && j > 0 && j <= a.k) close |= !gone(top) && !(prev - top >= tol + kTolChoice * fabs(prev));
             prev = top;
             if (q == j) picked = top;
@@ -661,10 +701,24 @@ bool launch_lanes(GateArgs& a, hipStream_t st) {
     constexpr int64_t kTokens = 4 * (64 / L);         // per workgroup
     // a launch takes up to kMaxRowGrid workgroups (a loop over tokens in the kernel would keep what is the same
     // for all of them in registers: 200 against 131 when tried)
+    //
+    // Sorted keys spend fewer instructions over many rounds, but in a longer chain: 256 experts on 16 lanes, k = 8, sigmoid,
+    // bias and groups, 16K tokens 14.7 us sorted and 15.5 not, 4096 tokens 8.0 and 7.7; 1024 experts on 64 lanes, 4096 tokens
+    // 13.5 and 14.6; 16K tokens with 2 rounds 7.7 and 7.4, 6 rounds 9.5 and 9.7.  So: where a SIMD has more than two waves.
+    const int rounds = a.balance != nullptr ? a.k + 2 : a.k;
+    const bool sorted = PL == 16 && rounds >= 6 && a.T * L / 64 > 2048;
     for (a.first = 0; a.first < a.T; a.first += kMaxRowGrid * kTokens) {
         const dim3 grid((unsigned)std::min<int64_t>((a.T - a.first + kTokens - 1) / kTokens, kMaxRowGrid));
-        if (a.part != nullptr) hipLaunchKernelGGL((gate_lanes_kernel<L, PL, true>), grid, dim3(256), lds, st, a);
-        else hipLaunchKernelGGL((gate_lanes_kernel<L, PL, false>), grid, dim3(256), lds, st, a);
+        auto launch = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), lds, st, a); };
+        if constexpr (PL == 16) {
+            if (sorted) {
+                if (a.part != nullptr) launch(gate_lanes_kernel<L, PL, true, true>);
+                else launch(gate_lanes_kernel<L, PL, false, true>);
+                continue;
+            }
+        }
+        if (a.part != nullptr) launch(gate_lanes_kernel<L, PL, true, false>);
+        else launch(gate_lanes_kernel<L, PL, false, false>);
     }
     return true;
 }

@@ -664,6 +664,24 @@ def test_few_and_many_tokens_choose_alike(E, groups, kept, top, k, score):
             check_gate(l, gate, balance, i2[:64], w2[:64])
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,top,k", [(256, 1, 1, 1, 8), (256, 8, 4, 2, 8), (160, 8, 3, 1, 6), (255, 5, 2, 2, 14), (130, 1, 1, 1, 4),
+                                                 (1024, 16, 4, 2, 8), (999, 1, 1, 1, 32)])
+def test_special_rows_among_many_thousands(E, groups, kept, top, k, score):
+    """The same with as many tokens as make the chip's issue rate the bound: NaN, infinities, ties, few live experts."""
+    g = gen(E + k)
+    l = special_rows(E, g)
+    many = l.repeat(160, 1)                             # 10240 rows
+    b = torch.randn(E, generator=g, device=DEV) * 0.05
+    b[E // 2] = -float("inf")
+    for balance in (None, b):
+        gate = make_gate(k, score, groups, kept, top, True, 1.5)
+        i1, w1 = run_gate(many, gate, balance)
+        check_gate(l, gate, balance, i1[:64], w1[:64])
+        assert torch.equal(i1.view(160, 64, k), i1[:64].expand(160, 64, k))
+        assert torch.equal(w1.view(160, 64, k), w1[:64].expand(160, 64, k))
+
+
 def torch_gate(l, gate, balance):
     """The gate's choice in fp64 by torch (finite logits)."""
     x = l.double()
