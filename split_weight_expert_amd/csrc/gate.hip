@@ -197,10 +197,11 @@ __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
 //
 // Precision.  Without a balance bias keys are the fp32 logits, exact.  Else they are choices from the
 // hardware's fp32 exponential and reciprocal, and every decision on them is checked against the error bounds
-// below.  Where the last group kept and the first one dropped are too close, the groups are ranked again by
-// the fp64 choices of their two best; where two consecutive picks are, the k picks and the next best, one per
-// lane, by theirs (one token in some hundreds of ordinary logits).  Where another expert is so close that it
-// could have taken part, gate_row_exact repeats the token.  So the choice is the fp64 one in every case.
+// below.  Where the value of a group that is kept and of one that is dropped, each within its own bound, could be the
+// other way round, the groups are ranked again by the fp64 choices of their two best; where two consecutive picks
+// could, the k picks and the next best, one per lane, by theirs (one token in some hundreds of ordinary logits).
+// Where another expert is so close that it could have taken part, gate_row_exact repeats the token.  So the choice is
+// the fp64 one in every case.
 //
 // Error bounds (u = 2^-24).  exp2 and rcp have errors of 2 u, products and sums 1 u.
 //   sigmoid: s = 1 / (1 + e), e = exp2(-l log2e): the exponent's error enters e relative by 1.5 |l| u, so s is
@@ -211,6 +212,9 @@ __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
 //     (2.1 + 2.23 ln E + 2 + log2 E + 3) u / S: 30 u / S up to 512 experts, 33 u / S up to 1024.
 //   the bias' addition adds u |c|.
 // Two keys: twice that.  kTol* are those sums rounded up to powers of two.
+//   a group's value b1 + b2 is off by twice a score's error, by u (|b1| + |b2|) from the biases and by u |b1 + b2| from
+//     its own sum.  Choices of both signs may leave a sum far smaller than they are, so the bound goes by |b1| + |b2|:
+//     kTol* + kTolChoice (|b1| + |b2|), of which at least 2 u (|b1| + |b2|) is left for the rounding of value +- bound.
 constexpr float kTolSigmoid = 0x1p-21f;       // >= 2 * 3.9 u
 constexpr float kTolSoftmax = 0x1p-18f;       // >= 2 * 30 u, times 1 / S
 constexpr float kTolSoftmax1024 = 0x1p-17f;   // >= 2 * 33 u, times 1 / S
@@ -312,6 +316,9 @@ constexpr Net16 kNet16;
 
 struct MaxF {
     __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct MinF {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); }
 };
 struct AddF {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
@@ -505,23 +512,27 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
             }
             const float value = pairs && b2 > f_neg_inf() ? b1 + b2 : b1;
             int before = 0;                           // groups ahead of this lane's
-            float next = f_neg_inf();                 // the best of the groups behind it
             for (int h = 0; h < a.groups; ++h) {
                 const float o = __shfl(value, h << a.lane_shift, L);
-                const bool ahead = o > value || (o == value && h < g);
-                before += ahead;
-                next = ahead || h == g ? next : fmaxf(next, o);
+                before += o > value || (o == value && h < g);
             }
-            // the last group kept looks at the first one dropped
-            const float margin = 2.0f * tol + 2.0f * kTolChoice * fabsf(value);
-            const bool last = before == a.kept - 1 && g < a.groups;
-            unsure = need_scores && last && next > f_neg_inf() && !(value - next >= margin);
+            kept = before < a.kept && g < a.groups;
+            // bounds of a group's value, and over the token the lowest of those kept and the highest of those dropped.  An
+            // infinite choice is exact, as its sum is; a sum that passes the largest fp32 number has no bound, and a group of no
+            // live expert none below.
+            const bool alive = b1 > f_neg_inf();
+            const float err = b1 == -f_neg_inf() ? 0.0f
+                                                 : tol + kTolChoice * (fabsf(b1) + (pairs && b2 > f_neg_inf() ? fabsf(b2) : 0.0f));
+            const bool bounded = err < -f_neg_inf();
+            const float low = bounded ? value - err : f_neg_inf(), high = bounded ? value + err : -f_neg_inf();
+            const float low_kept = need_scores ? over_token<L>(kept ? low : -f_neg_inf(), MinF()) : 0.0f;
+            const float high_dropped = need_scores ? over_token<L>(!kept && alive ? high : f_neg_inf(), MaxF()) : 0.0f;
+            unsure = need_scores && !(low_kept >= high_dropped);
             const unsigned long long who = __ballot(unsure);
             if (who != 0) {
                 logits_written();
                 // the same by fp64 values of each group's two best; where a third expert is so near that it may be
-                // one of them, in a group near the border, the token stays unsure
-                const float border = over_token<L>(last ? value : f_neg_inf(), MaxF());
+                // one of them, in a group whose bounds reach past the border, the token stays unsure
                 double k1 = make_key(c[0], base), k2 = from32(kGoneHi, 0);
 #pragma unroll
                 for (int i = 1; i < PL; ++i) {
@@ -538,7 +549,7 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
                 bool third = false;
 #pragma unroll
                 for (int i = 0; i < PL; ++i)
-                    third |= c[i] > f_neg_inf() && base + i != e1 && base + i != e2 && !((pairs ? b2 : b1) - c[i] >= margin);
+                    third |= c[i] > f_neg_inf() && base + i != e1 && base + i != e2 && !((pairs ? b2 : b1) - c[i] >= err);
                 const double total = a.sigmoid ? 1.0 : softmax_total(who, t0, m);
                 const double c1 = gone(k1) ? -__builtin_huge_val() : choice64(t, e1, m, total);
                 const double c2 = gone(k2) ? -__builtin_huge_val() : choice64(t, e2, m, total);
@@ -548,11 +559,11 @@ __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
                     const double o = __shfl(v, h << a.lane_shift, L);
                     before64 += o > v || (o == v && h < g);
                 }
-                const bool again = (who & (kToken << (lane & ~(L - 1)))) != 0;   // this token; no other has a total
-                before = again ? before64 : before;
-                unsure = again && third && !(fabsf(value - border) >= 2.0f * margin);
+                // of this token's lanes, all or none are unsure; no other token has a total
+                const bool near = kept ? !(low >= high_dropped) : !(low_kept >= high);
+                if (unsure) kept = before64 < a.kept && g < a.groups;
+                unsure = unsure && third && near;
             }
-            kept = before < a.kept && g < a.groups;
         }
         double key[PL];
 #pragma unroll
