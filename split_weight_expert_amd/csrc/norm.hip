@@ -206,7 +206,8 @@ __device__ __forceinline__ void load_z(const NormArgs& a, int64_t t, int col, co
 
 // Rows too wide for the registers (above 32768 elements; combine above 16384): one workgroup per row, which reads z
 // twice (for the sum of squares, then to write), each element by the same thread, so that outputs may take their
-// inputs' place.
+// inputs' place.  Columns are counted without a sign: the step past the last one of a row of nearly 2^31 elements is
+// still a number that lies behind the row.
 template <bool COMBINE, bool BF16, bool EVEN>
 __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
     __shared__ int32_t s_row[kMaxK];
@@ -222,7 +223,7 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
         }
         __syncthreads();
         float ss = 0.0f, z[8];
-        for (int c = tid * 8; c < a.H; c += 256 * 8) {
+        for (uint32_t c = tid * 8; c < (uint32_t)a.H; c += 256 * 8) {
             load_z<COMBINE, BF16, EVEN>(a, t, c, s_row, s_w, z);
 #pragma unroll
             for (int u = 0; u < 8; ++u) ss += z[u] * z[u];
@@ -232,7 +233,7 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
         __syncthreads();
         ss = (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
         const float r = 1.0f / sqrtf(ss / (float)a.H + a.eps);
-        for (int c = tid * 8; c < a.H; c += 256 * 8) {
+        for (uint32_t c = tid * 8; c < (uint32_t)a.H; c += 256 * 8) {
             load_z<COMBINE, BF16, EVEN>(a, t, c, s_row, s_w, z);
             finish8<BF16, EVEN>(a, t, c, z, r);
         }
