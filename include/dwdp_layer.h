@@ -89,7 +89,7 @@ int dwdp_gate_topk(const float* logits, const float* balance_bias, int64_t T, in
  *   128 columns scale = amax/448 (1 when amax is 0, 2^-126 where amax/448 is less), code = E4M3(n/scale)
  *   (NULL, both: not written)
  * At least one of y and q is given.  Non-finite values follow IEEE arithmetic; a NaN in a 128-column
- * group makes its scale and its codes NaN.  z^2 is summed in fp32: rows whose sum of squares passes
+ * group makes its scale and its codes NaN.  The sum of z^2 has fp32's range: rows whose sum of squares passes
  * 3.4e38 norm to zero, and with eps 0 a row whose squares all underflow norms to infinities and NaN.
  *   x, residual, sum_out, y [T,H] of dtype (DWDP_F32 or DWDP_BF16); weight [H] of w_dtype (DWDP_F32 or
  *   DWDP_BF16).  Any H >= 1 and any element-aligned pointers; rows are read fastest where

@@ -60,3 +60,33 @@ def test_combine_add_rmsnorm_of_the_widest_row():
                             sum_out=so)
     torch.cuda.synchronize()
     check(H, z, so, None, None, 0.0)
+
+
+@pytest.mark.parametrize("dt,H", [("f32", 33000), ("f32", 1 << 20), ("f32", (1 << 25) + 3), ("f32", (1 << 30) + 8), ("bf16", (1 << 31) - 8)])
+def test_a_wide_row_of_equal_elements(dt, H):
+    """Terms that are all alike round all the same way once the sum is far larger than each: the mean square of a row
+    of 1.09375 (its square is exact) is off by the roundings of 7 additions in a vector, of the sum to fp32, of 8
+    additions in the workgroup, of H and of the division, half of which (9 u) are on the root; the root, its reciprocal
+    and the product with z add 3 u, and the output its rounding."""
+    from split_weight_expert_amd import api
+    t = {"f32": torch.float32, "bf16": torch.bfloat16}[dt]
+    x = torch.full((1, H), 1.09375, dtype=t, device=DEV)
+    w = torch.ones(H, dtype=t, device=DEV)
+    y = torch.empty_like(x)
+    api.add_rmsnorm(x, None, w, 0.0, y=y)
+    torch.cuda.synchronize()
+    u = 2.0 ** -24
+    low, high = float(y.min()), float(y.max())
+    tol = 12 * u + (UB16 if dt == "bf16" else u)
+    assert 1 - tol <= low and high <= 1 + tol, (low, high)
+
+
+def test_a_wide_boundary_of_equal_elements():
+    from split_weight_expert_amd import api
+    H = 1 << 24
+    x = torch.full((3, H), 0.546875, device=DEV)
+    inv = torch.tensor([[0, 1]], dtype=torch.int32, device=DEV)
+    y = torch.empty(1, H, device=DEV)
+    api.combine_add_rmsnorm(x, inv, torch.full((1, 2), 0.5, device=DEV), 1, None, torch.ones(H, device=DEV), 0.0, y=y)
+    torch.cuda.synchronize()
+    assert float((y.double() - 1).abs().max()) <= 13 * 2.0 ** -24
