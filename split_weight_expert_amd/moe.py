@@ -193,8 +193,8 @@ class MoEBlock:
         api.route_topk(x, w_router, bias, self.k, b.logits, b.idx, b.w, stream)
 
     def permute(self, x, b: BlockBuffers, stream=None):
-        b.normed = False                      # fp8: the codes below take the normed ones' place
         """Expert permutation; gather mode also writes x_perm, token mode quantises the tokens for fp8."""
+        b.normed = False                      # fp8: the codes below take the normed ones' place
         fp8 = self.w_dtype == FP8_E4M3
         api.permute(b.idx, self.E, self.shared, x, self.w_dtype if fp8 else api.dtype_code(x),
                     b.x_perm, b.x_perm_scale, b.offsets, b.perm_src, b.inv_perm, b.ws_perm, stream)
