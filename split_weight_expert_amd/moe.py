@@ -239,6 +239,7 @@ class MoEBlock:
 
     def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None):
         """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given)."""
+        b.normed = False                      # a refused norm is none, whatever was there before
         api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b))
         b.normed = True
 

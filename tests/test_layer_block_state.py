@@ -37,3 +37,17 @@ def rows(T=4):
 def test_methods_have_their_docstrings():
     for name in ("forward", "permute", "norm", "forward_normed"):
         assert getattr(MoEBlock, name).__doc__, name
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8"])
+def test_a_norm_refused_after_another_is_none(calls, dtype):
+    blk = block(dtype)
+    x, w, b = rows(), torch.ones(256), blk.buffers(4)
+    blk.norm(x, w, 1e-6, b)
+    blk.forward_normed(x, None, None, None)
+    blk.norm(x, w, 1e-6, b)
+    calls.refuse = ("add_rmsnorm",)
+    with pytest.raises(ValueError, match="add_rmsnorm refused"):
+        blk.norm(x, w, 1e-6, b)
+    with pytest.raises(ValueError, match="no normed input"):
+        blk.forward_normed(x, None, None, None)
