@@ -19,6 +19,7 @@ from __future__ import annotations
 from dataclasses import dataclass
 
 import torch
+from torch.multiprocessing.reductions import StorageWeakRef
 
 from . import api
 from ._lib import BF16, F32, FP8_E4M3
@@ -114,6 +115,27 @@ def dwdp_placement(E: int, n_local: int, shared: int, slot_set: int = 1):
     return pl
 
 
+class Normed:
+    """One normed input in a block's buffers: a handle to it, and the tensor it is the norm of.
+
+    The tensor is known by its memory, which is not kept alive (memory that was freed is no tensor's any more), and by
+    torch's count of the writes to it, as long as torch counts them (it does not for inference tensors)."""
+
+    def __init__(self, source: torch.Tensor | None):
+        self._memory = None if source is None else (StorageWeakRef(source.untyped_storage()), source.data_ptr())
+        self._writes = None if source is None else self._count(source)
+
+    @staticmethod
+    def _count(t):
+        return None if t.is_inference() else t._version
+
+    def shares_memory(self, t: torch.Tensor) -> bool:
+        return self._memory is not None and (StorageWeakRef(t.untyped_storage()), t.data_ptr()) == self._memory
+
+    def is_of(self, t: torch.Tensor) -> bool:
+        return self.shares_memory(t) and self._count(t) == self._writes
+
+
 @dataclass
 class BlockBuffers:
     logits: torch.Tensor
@@ -133,7 +155,7 @@ class BlockBuffers:
     x_tokens: torch.Tensor | None = None  # token mode: the rows GEMM1 reads (x, or x_q for fp8)
     ws_route: torch.Tensor | None = None  # workspace of the gate's router product (None: it needs none)
     x_norm: torch.Tensor | None = None    # normed layers: the block's input, written by the norm before it
-    normed: bool = False                  # x_norm (and for fp8 x_q) hold a normed input that no forward() replaced
+    normed: Normed | None = None          # the normed input in x_norm (and for fp8 x_q), unless forward() replaced it
 
 
 class MoEBlock:
@@ -194,7 +216,7 @@ class MoEBlock:
 
     def permute(self, x, b: BlockBuffers, stream=None):
         """Expert permutation; gather mode also writes x_perm, token mode quantises the tokens for fp8."""
-        b.normed = False                      # fp8: the codes below take the normed ones' place
+        b.normed = None                       # fp8: the codes below take the normed ones' place
         fp8 = self.w_dtype == FP8_E4M3
         api.permute(b.idx, self.E, self.shared, x, self.w_dtype if fp8 else api.dtype_code(x),
                     b.x_perm, b.x_perm_scale, b.offsets, b.perm_src, b.inv_perm, b.ws_perm, stream)
@@ -230,26 +252,40 @@ class MoEBlock:
 
     # A pre-norm layer is h' = h + block(norm(h)).  The norm of a layer's input is written by `norm` (a
     # model's first layer) or by the layer before it (forward_normed's next_weight), into b.x_norm and, for
-    # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.
+    # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.  All batches of one
+    # size share these buffers, so forward_normed asks whose norm they hold.
 
     def _norm_outputs(self, b: BlockBuffers):
         if b.x_norm is None:
             b.x_norm = torch.empty_like(b.y)
         return dict(y=b.x_norm, q=b.x_q, q_scale=b.x_q_scale)
 
-    def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None):
-        """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given)."""
-        b.normed = False                      # a refused norm is none, whatever was there before
+    def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None) -> Normed:
+        """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given).
+
+        That forward_normed is called with the normed tensor, which is sum_out if given and else x; or with the handle
+        returned here, which it needs after a norm of x + residual whose sum went nowhere."""
+        b.normed = None                       # a refused norm is none, whatever was there before
         api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b))
-        b.normed = True
+        b.normed = Normed(sum_out if sum_out is not None else x if residual is None else None)
+        return b.normed
 
     def forward_normed(self, h, w_router, bias, table, next_weight=None, eps: float = 1e-6, stream=None, out=None,
-                       balance_bias=None) -> BlockBuffers:
+                       balance_bias=None, normed: Normed | None = None) -> BlockBuffers:
         """A layer whose normed input is in the buffers: h + block(b.x_norm) to `out` (b.y if not given; h itself
-        works), and with next_weight that sum's norm to the buffers, the next layer's input."""
+        works), and with next_weight that sum's norm to the buffers, the next layer's input.
+
+        The buffers must hold the norm of h: that of another tensor, or of what h was before torch wrote to it, is
+        refused (another batch of the same size may have been normed since).  With `normed`, the handle of the normed
+        input (norm()'s result, or b.normed after the layer before), any h is taken as long as that input is there."""
         b = self.buffers(h.shape[0])
-        if not b.normed:
+        if b.normed is None:
             raise ValueError("no normed input: call norm() on the buffers first")
+        if normed is not None and normed is not b.normed:
+            raise ValueError("no normed input of this handle: the buffers hold another one")
+        if normed is None and not b.normed.is_of(h):
+            raise ValueError("no normed input of this h: the buffers hold that of another tensor, or of an earlier content; "
+                             "call norm() on h, or pass the handle of the normed input")
         self.route(b.x_norm, w_router, bias, b, stream, balance_bias)
         api.permute(b.idx, self.E, self.shared, b.x_norm,
                     self.w_dtype if self.w_dtype == FP8_E4M3 else api.dtype_code(b.x_norm), b.x_perm, b.x_perm_scale,
@@ -257,9 +293,15 @@ class MoEBlock:
         if not self.gather:
             b.x_tokens = b.x_norm if b.x_q is None else b.x_q
         self.ffn(table, b, stream)
-        api.combine_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, next_weight, eps,
-                                sum_out=b.y if out is None else out, stream=stream,
+        out = b.y if out is None else out
+        now, b.normed = b.normed, None
+        api.combine_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, next_weight, eps, sum_out=out, stream=stream,
                                 **(self._norm_outputs(b) if next_weight is not None else {}))
+        if next_weight is not None:
+            b.normed = Normed(out)
+        elif (not now.shares_memory(out) and out.data_ptr() != h.data_ptr() and
+              out.untyped_storage().data_ptr() != b.x_norm.untyped_storage().data_ptr()):
+            b.normed = now                    # neither x_norm nor what it is the norm of was written
         return b
 
 
@@ -397,12 +439,13 @@ class DWDPPipeline:
             lw = layers[l]
             if normed:
                 if l == 0:
-                    self.block.norm(x, lw.norm, lw.norm_eps, self.block.buffers(T))
+                    handle = self.block.norm(x, lw.norm, lw.norm_eps, self.block.buffers(T))
                 nxt = layers[l + 1] if l + 1 < L else None
                 b = self.block.forward_normed(x, lw.w_router, lw.bias, self.table(lw, s),
                                               next_weight=None if nxt is None else nxt.norm,
                                               eps=lw.norm_eps if nxt is None else nxt.norm_eps, out=outputs[l],
-                                              balance_bias=lw.balance_bias)
+                                              balance_bias=lw.balance_bias, normed=handle)
+                handle = b.normed
             else:
                 b = self.block.forward(x, lw.w_router, lw.bias, self.table(lw, s), out=outputs[l],
                                        balance_bias=lw.balance_bias)
