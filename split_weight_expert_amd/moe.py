@@ -16,6 +16,7 @@ Nothing here computes: every step is a libdwdp call.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass
 
 import torch
@@ -255,9 +256,11 @@ class MoEBlock:
     # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.  All batches of one
     # size share these buffers, so forward_normed asks whose norm they hold.
 
-    def _norm_outputs(self, b: BlockBuffers):
+    def _norm_outputs(self, b: BlockBuffers, stream=None):
         if b.x_norm is None:
-            b.x_norm = torch.empty_like(b.y)
+            # on the stream that writes it first: the allocator may give memory whose last reader on another is not done
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+                b.x_norm = torch.empty_like(b.y)
         return dict(y=b.x_norm, q=b.x_q, q_scale=b.x_q_scale)
 
     def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None) -> Normed:
@@ -266,7 +269,7 @@ class MoEBlock:
         That forward_normed is called with the normed tensor, which is sum_out if given and else x; or with the handle
         returned here, which it needs after a norm of x + residual whose sum went nowhere."""
         b.normed = None                       # a refused norm is none, whatever was there before
-        api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b))
+        api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b, stream))
         b.normed = Normed(sum_out if sum_out is not None else x if residual is None else None)
         return b.normed
 
@@ -296,7 +299,7 @@ class MoEBlock:
         out = b.y if out is None else out
         now, b.normed = b.normed, None
         api.combine_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, next_weight, eps, sum_out=out, stream=stream,
-                                **(self._norm_outputs(b) if next_weight is not None else {}))
+                                **(self._norm_outputs(b, stream) if next_weight is not None else {}))
         if next_weight is not None:
             b.normed = Normed(out)
         elif (not now.shares_memory(out) and out.data_ptr() != h.data_ptr() and

@@ -55,3 +55,21 @@ def test_batches_of_one_size_do_not_mix(dt, gather):
     blk.forward_normed(x, wr, b, table, out=out)
     assert torch.equal(out, want["x"])
     del store
+
+
+def test_the_first_norm_on_a_side_stream():
+    """x_norm's memory is not one that the current stream, far behind, still reads from a tensor freed on it."""
+    from split_weight_expert_amd import MoEBlock
+    T, H = 512, 2048
+    blk = MoEBlock(H, 256, 8, 2, 0, "bf16", DEV)
+    bb = blk.buffers(T)
+    x, w = torch.ones(T, H, dtype=torch.bfloat16, device=DEV), torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    old, keep = torch.full_like(x, 3), torch.zeros_like(x)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    keep.copy_(old)
+    del old                                            # reads it only after the sleep
+    blk.norm(x, w, 0.0, bb, stream=side)
+    torch.cuda.synchronize()
+    assert (keep == 3).all() and (bb.x_norm == 1).all()
