@@ -253,8 +253,10 @@ class MoEBlock:
 
     # A pre-norm layer is h' = h + block(norm(h)).  The norm of a layer's input is written by `norm` (a
     # model's first layer) or by the layer before it (forward_normed's next_weight), into b.x_norm and, for
-    # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.  All batches of one
-    # size share these buffers, so forward_normed asks whose norm they hold.
+    # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.  fp8 layers in gather
+    # mode quantise the rows of b.x_norm as they gather them, as forward() does its tokens: their codes are those of the
+    # norm rounded to bf16, the others' of the unrounded norm, so the two modes differ by that rounding.  All batches of
+    # one size share these buffers, so forward_normed asks whose norm they hold.
 
     def _norm_outputs(self, b: BlockBuffers, stream=None):
         if b.x_norm is None:

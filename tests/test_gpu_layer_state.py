@@ -1,11 +1,14 @@
-"""Pre-norm layers of MoEBlock on the GPU, whose buffers all batches of one size share."""
+"""Pre-norm layers of MoEBlock on the GPU, whose buffers all batches of one size share, and in gather mode."""
+import numpy as np
 import pytest
 import torch
 
 import synth
+from oracle import moe as omoe
 from synth.configs import shrink
-from tests.gpu_util import HostLayer, need_gpu, upload_layer
-from tests.test_gpu_layer_block import CASES, DEV, make_gate
+from tests.gpu_util import HostLayer, assert_close, need_gpu, to_np, upload_layer
+from tests.test_gpu_layer import U32, check_norm
+from tests.test_gpu_layer_block import CASES, DEV, make_gate, oracle_gate
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +76,50 @@ def test_the_first_norm_on_a_side_stream():
     blk.norm(x, w, 0.0, bb, stream=side)
     torch.cuda.synchronize()
     assert (keep == 3).all() and (bb.x_norm == 1).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "fp8"])
+def test_two_prenorm_layers_in_gather_mode(dt):
+    """Both layers of a pair against the oracle on the GPU's own input of that layer; the second one's norm comes from
+    the first one's boundary.  Codes of fp8 rows are the token quantiser's of the normed rows."""
+    from split_weight_expert_amd import api
+    cfg, hl, blk, store, table, x, wr, b = layer(dt, gather=True)
+    g = torch.Generator().manual_seed(3)
+    w = [(1 + 0.2 * torch.randn(cfg.H, generator=g)).to(DEV, x.dtype) for _ in range(2)]
+    bb = blk.buffers(cfg.T)
+    h = [x, torch.empty_like(x), torch.empty_like(x)]
+    blk.norm(x, w[0], 1e-6, bb)
+    for l in range(2):
+        xn = bb.x_norm.clone()
+        z = to_np(h[l]).astype(np.float64)
+        # the boundary normed the unrounded sum: half a step of the type from the stored one
+        z_err = np.abs(z) * (0 if l == 0 else U32 if dt == "f32" else 2.0 ** -8)
+        check_norm(z, z_err, w[l].double().cpu().numpy(), 1e-6, "f32" if dt == "f32" else "bf16", y=xn)
+        blk.forward_normed(h[l], wr, b, table, next_weight=w[1] if l == 0 else None, out=h[l + 1])
+        torch.cuda.synchronize()
+        lg = bb.logits.cpu().numpy()
+        oi, ow = oracle_gate(blk.gate, lg, None)
+        np.testing.assert_array_equal(bb.idx.cpu().numpy(), oi)
+        if dt == "fp8":
+            q, s = torch.empty(cfg.T, cfg.H, dtype=torch.uint8, device=DEV), torch.empty(cfg.T, cfg.H // 128, device=DEV)
+            api.quantize_tokens_fp8(xn, q, s)
+            src = bb.perm_src.long()
+            assert torch.equal(bb.x_perm, q[src]) and torch.equal(bb.x_perm_scale, s[src])
+        ref = omoe.moe_layer(to_np(xn).astype(np.float32), hl.wr, hl.bias, cfg.k, lambda e: hl.experts[e], lambda: hl.shared,
+                             precision=dt, routing=(lg, oi, ow))
+        assert_close(to_np(h[l + 1]), z + ref["y"], dt, f"layer {l} ({dt}, gather)")
+    del store
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_both_modes_of_a_normed_layer_give_the_same_bits(dt):
+    outs = []
+    for gather in (False, True):
+        cfg, _, blk, store, table, x, wr, b = layer(dt, gather)
+        blk.norm(x, torch.ones(cfg.H, dtype=x.dtype, device=DEV), 1e-6, blk.buffers(cfg.T))
+        out = torch.empty_like(x)
+        blk.forward_normed(x, wr, b, table, out=out)
+        torch.cuda.synchronize()
+        outs.append(out)
+        del store
+    assert torch.equal(*outs)
