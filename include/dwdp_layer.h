@@ -65,7 +65,9 @@ typedef struct {
  *   logits_out [T,E] fp32 (written, bias included), topk_idx [T,k] int32, topk_w [T,k] fp32.
  *   ws: dwdp_route_gate_workspace_bytes(...) bytes of device scratch, 16-byte aligned (NULL if 0); its
  *   contents need no preparation and mean nothing after the call.  Calls that may run at the same time
- *   need a workspace each.
+ *   need a workspace each.  The size is that of exactly these T, H, E and in_dtype, whatever the gate: a larger T
+ *   may need less, or none.  It is never more than DWDP_ROUTE_GATE_WORKSPACE_MAX, and a larger ws is taken, so one
+ *   buffer of that size serves every batch of a stream.
  *   No output, nor ws, may overlap another buffer.  T is limited by one launch of the product: more than 10^8
  *   tokens of 256 experts (f32 with H % 32 != 0: 8 * 10^6); larger batches are refused. */
 int dwdp_route_gate(const void* x, const void* w_router, int in_dtype, const float* bias,
@@ -74,6 +76,7 @@ int dwdp_route_gate(const void* x, const void* w_router, int in_dtype, const flo
                     void* stream);
 
 /* Device scratch dwdp_route_gate needs (0 where it needs none, and for arguments it rejects). */
+#define DWDP_ROUTE_GATE_WORKSPACE_MAX ((size_t)32 << 20)
 size_t dwdp_route_gate_workspace_bytes(int64_t T, int H, int E, int in_dtype);
 
 /* The gate alone: logits [T,E] fp32 -> topk_idx [T,k], topk_w [T,k], neither of which may overlap another buffer. */

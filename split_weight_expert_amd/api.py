@@ -262,7 +262,12 @@ _I32 = (torch.int32,)
 _U8 = (torch.uint8,)
 
 
+ROUTE_GATE_WORKSPACE_MAX = 32 << 20
+
+
 def route_gate_workspace_bytes(T: int, H: int, E: int, dtype: int) -> int:
+    """Bytes of route_gate's workspace for exactly these sizes (a larger T may need less, or none); a larger workspace is
+    taken, and ROUTE_GATE_WORKSPACE_MAX bytes are enough for any."""
     return int(_lib.load().dwdp_route_gate_workspace_bytes(T, H, E, dtype))
 
 

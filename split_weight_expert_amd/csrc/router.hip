@@ -274,6 +274,7 @@ RouterPlan plan_router(int64_t T, int H, int E, int dtype) {
     }
     const int64_t tiles = ceil_div(T, p.bm) * ceil_div(E, p.bn);
     const int64_t most = p.bm == 16 ? std::min<int64_t>(4, row_bytes / 64 / 16) : std::min<int64_t>(8, row_bytes / 128 / 8);
+    // slices * tiles <= want, so the slices' sums are at most want * bm * bn numbers: 32 MiB with the widest tiles
     p.slices = (int)std::max<int64_t>(1, std::min(want / tiles, most));
     return p;
 }

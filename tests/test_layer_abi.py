@@ -272,3 +272,18 @@ def test_pipeline_refuses_mixed_norms():
             p.forward(torch.zeros(2, 4), lw)
         with pytest.raises(ValueError, match="chain"):
             p.forward(torch.zeros(2, 4), lw[:1], chain=False)
+
+
+def test_one_workspace_serves_every_batch(lib):
+    """The size is not monotonic in T, but bounded: a buffer of the bound is taken for every batch."""
+    from split_weight_expert_amd import api
+    text = open(HEADER).read()
+    assert "DWDP_ROUTE_GATE_WORKSPACE_MAX ((size_t)32 << 20)" in text and api.ROUTE_GATE_WORKSPACE_MAX == 32 << 20
+    need = [lib.dwdp_route_gate_workspace_bytes(T, 7168, 256, 1) for T in (64, 8192, 10000, 16384, 32768)]
+    assert need[1] > need[2] > 0 and need[4] == 0
+    ts = sorted({min(max(b + d, 1), 1 << 21) for p in range(22) for b in (1 << p, 5 << p) for d in (-1, 0, 1)})
+    for dt, hs in ((1, (64, 1984, 7168, 16384, 1 << 20)), (0, (16, 1040, 7168, 1 << 20))):
+        for H in hs:
+            for E in (1, 16, 60, 64, 65, 128, 129, 256, 257, 320, 512, 513, 1000, 1024):
+                for T in ts:
+                    assert lib.dwdp_route_gate_workspace_bytes(T, H, E, dt) <= api.ROUTE_GATE_WORKSPACE_MAX, (T, H, E, dt)
