@@ -123,3 +123,26 @@ def test_both_modes_of_a_normed_layer_give_the_same_bits(dt):
         outs.append(out)
         del store
     assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_a_normed_layer_without_a_gate(dt, gather):
+    """The plain top-k's block inside a residual layer is forward() on the normed rows, and the residual: the boundary adds
+    it in fp32 and rounds once, forward() rounds its own sum first."""
+    from split_weight_expert_amd import MoEBlock
+    cfg, _, _, store, table, x, wr, b = layer(dt, gather)
+    blk = MoEBlock(cfg.H, cfg.I, cfg.E, cfg.k, cfg.shared, cfg.dtype, DEV, gather=gather)
+    blk.norm(x, torch.ones(cfg.H, dtype=x.dtype, device=DEV), 1e-6, blk.buffers(cfg.T))
+    out = torch.empty_like(x)
+    bb = blk.forward_normed(x, wr, b, table, out=out)
+    idx, xn = bb.idx.clone(), bb.x_norm.clone()
+    y = torch.empty_like(x)
+    blk.forward(xn, wr, b, table, out=y)
+    torch.cuda.synchronize()
+    assert torch.equal(idx, bb.idx)
+    u = 2.0 ** -8 if dt == "bf16" else U32
+    want = x.double() + y.double()
+    # y's rounding, the fp32 addition, the output's rounding
+    assert ((out.double() - want).abs() <= u * y.double().abs() + (u + U32) * (1 + u) * (want.abs() + u * y.double().abs())).all()
+    del store
