@@ -176,7 +176,8 @@ __device__ void gate_row_exact(const GateArgs& a, int64_t t, double* c) {
 
 // One wave per token, 4 tokens per workgroup; a bounded grid walks the tokens.  Taken by gates that no lane layout of
 // gate_lanes_kernel holds (more than 64 groups, or groups of more than 16 experts a lane).  Bound by fp64 exponentials
-// and by the shuffles of the top-k's rounds: 16K tokens x 256 experts, k = 8, 8 groups took 57 us here.
+// and by the shuffles of the top-k's rounds: 16K tokens, k = 8, sigmoid and bias: 256 experts in 128 groups 85 us, 1000 in 5
+// groups 235 (in 8 groups, which gate_lanes_kernel holds, 45); one token of the latter 35 us and 7.
 template <int PL>
 __global__ __launch_bounds__(256) void gate_exact_kernel(GateArgs a) {
     extern __shared__ double lds[];
@@ -332,7 +333,7 @@ struct MaxKey {
 
 // Bound by instruction issue: 16K tokens x 256 experts (sigmoid, bias, 4 of 8 groups, k = 8) are 18 MB, 3.6 us of
 // memory traffic, and 1200 vector instructions for each four tokens, 8.0 us if every SIMD issued one every four
-// cycles without a pause; 14.9 us measured in a graph, other inputs in between, of which a launch takes 2.3.  Not
+// cycles without a pause; 15.4 us measured in a graph, other inputs in between, of which a launch takes 2.3.  Not
 // faster: keeping the logits in LDS instead of reading the chosen ones again (2 us more), or taking them from the
 // lanes that hold them (0.2 us more at every size).
 //
@@ -340,7 +341,7 @@ struct MaxKey {
 // others, as far as later rounds can look, in place of 15 maxima and 16 comparisons with their selections.
 //
 // SLICED: the logits come as a router product's partial sums, and are written on the way; lanes that repeat the last
-// token write the same values.  4 slices of 8192 x 256 (34 MB): 17 us, against 10 us from logits.
+// token write the same values.  4 slices of 8192 x 256 (34 MB): 17 to 18 us, against 10 us from logits.
 template <int L, int PL, bool SLICED, bool SORTED>
 __global__ __launch_bounds__(256, 2) void gate_lanes_kernel(GateArgs a) {
     constexpr int TPW = 64 / L;                       // tokens per wave
@@ -713,9 +714,10 @@ bool launch_lanes(GateArgs& a, hipStream_t st) {
     // a launch takes up to kMaxRowGrid workgroups (a loop over tokens in the kernel would keep what is the same
     // for all of them in registers: 200 against 131 when tried)
     //
-    // Sorted keys spend fewer instructions over many rounds, but in a longer chain: 256 experts on 16 lanes, k = 8, sigmoid,
-    // bias and groups, 16K tokens 14.7 us sorted and 15.5 not, 4096 tokens 8.0 and 7.7; 1024 experts on 64 lanes, 4096 tokens
-    // 13.5 and 14.6; 16K tokens with 2 rounds 7.7 and 7.4, 6 rounds 9.5 and 9.7.  So: where a SIMD has more than two waves.
+    // Sorted keys spend fewer instructions over many rounds, but in a longer chain (20 inputs in turn in a graph): 256 experts
+    // on 16 lanes, k = 8, sigmoid, bias and groups, 16K tokens 15.4 us sorted and 16.2 not, 4096 tokens 9.0 and 8.9; 1024
+    // experts on 64 lanes, 4096 tokens 16.1 and 17.3; 16K tokens with 2 rounds 8.3 and 7.9, 6 rounds 9.4 and 9.8.  So: where a
+    // SIMD has more than two waves.
     const int rounds = a.balance != nullptr ? a.k + 2 : a.k;
     const bool sorted = PL == 16 && rounds >= 6 && a.T * L / 64 > 2048;
     for (a.first = 0; a.first < a.T; a.first += kMaxRowGrid * kTokens) {
@@ -752,10 +754,10 @@ bool lanes_hold(const GateArgs& a) {
 int launch_gate(GateArgs a, hipStream_t st) {
     if (lanes_hold(a)) {
         // The narrowest layout that holds it: four tokens to a wave spend fewer instructions on each, 64 lanes on one
-        // are done sooner as long as the chip has room for the waves.  16 against 64 lanes, us:
-        //   4 experts a lane (64 experts, k = 8): 1 token 3.0 and 3.3, 1777 tokens 3.5 and 4.3
-        //   8 (128, sigmoid with a bias):         64 tokens 4.5 and 4.3, 1777 4.7 and 4.8, 4096 5.0 and 6.0
-        //   16 (256, the same and 4 of 8 groups): 64 tokens 6.8 and 5.4, 2048 7.0 and 6.0, 3500 7.4 and 8.1
+        // are done sooner as long as the chip has room for the waves.  16 against 64 lanes, us, 20 inputs in turn in a graph:
+        //   4 experts a lane (64 experts, k = 8): 1 token 3.2 and 3.4, 1777 tokens 3.6 and 4.3
+        //   8 (128, sigmoid with a bias):         64 tokens 4.5 and 4.4, 1777 5.2 and 5.4, 4096 6.1 and 7.8
+        //   16 (256, the same and 4 of 8 groups): 64 tokens 6.7 and 5.2, 2048 8.4 and 7.0, 3500 8.7 and 8.7
         launch_lanes<16, 4>(a, st) || (a.T > 1024 && launch_lanes<16, 8>(a, st)) ||
             (a.T > 2048 && launch_lanes<16, 16>(a, st)) || launch_lanes<64, 4>(a, st) || launch_lanes<64, 8>(a, st) ||
             launch_lanes<64, 16>(a, st);

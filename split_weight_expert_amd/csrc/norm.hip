@@ -252,8 +252,8 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
 //
 // Bound by HBM: each input is read and each output written once (counted).  7168-wide bf16 rows, residual, sum, y and
 // codes: 16384 rows are 1061 MB in 184 us, 5.8 TB/s; combine of 8192 rows, k = 8 and a shared row, 1470 MB in 271 us,
-// 5.4 TB/s (a plain copy reaches 4.9).  A few rows are bound by latency: one row 3.8 us, of which an empty
-// kernel takes 2.3.  Reading the rows twice (norm_two_pass_kernel) took 241 us and 495 us.
+// 5.4 TB/s (a plain copy reaches 4.9); fp32 rows, sum and y: 4096 tokens 1409 MB in 298 us, 4.7 TB/s.  A few rows are
+// bound by latency: one row 3.8 us, of which an empty kernel takes 2.3.  Reading the rows twice (norm_two_pass_kernel) took 241 us and 495 us.
 template <bool COMBINE, bool BF16, bool EVEN, int C, int LANES>
 __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
     static_assert(!COMBINE || EVEN, "combine takes rows of a multiple of 8");
