@@ -136,6 +136,9 @@ class Normed:
     def is_of(self, t: torch.Tensor) -> bool:
         return self.shares_memory(t) and self._count(t) == self._writes
 
+    def __reduce__(self):
+        return Normed, (None,)                # a copy of the buffers is another's: it knows no tensor, and owns no reference
+
 
 @dataclass
 class BlockBuffers:

@@ -186,3 +186,24 @@ def test_a_refused_boundary_leaves_no_normed_input(calls):
         forward(blk, x)
     calls.refuse = ()
     refused(calls, blk, x)
+
+
+def test_copies_of_a_block(calls):
+    """A copied or stored normed input knows no tensor: its own handle is needed, and nothing is freed twice."""
+    import copy
+    import io
+    import pickle
+    blk = block()
+    x, w, b = rows(), torch.ones(256), blk.buffers(4)
+    n = blk.norm(x, w, 1e-6, b)
+    f = io.BytesIO()
+    pickle.dump(n, f)
+    assert n._memory is not None and pickle.loads(f.getvalue())._memory is None and copy.copy(n)._memory is None
+    other = copy.deepcopy(blk)
+    o = other.buffers(4).normed
+    assert o is not n and o._memory is None
+    refused(calls, other, x)
+    refused(calls, other, x, normed=n)
+    forward(other, x, normed=o)
+    del other, o
+    forward(blk, x)
