@@ -45,9 +45,11 @@
  *   w_router   [E, H]            router weight, same dtype as x
  *   expert e   W13 [2I, H]       gate rows 0..I-1, then up rows (Wg stacked on Wu)
  *              W2  [H, I]        down projection
- *              (f32: row-major; bf16 / fp8: fragment-major, see dwdp_pack_weights)
- *              fp8 only: S13 [2I/128, H/128] and S2 [H/128, I/128] fp32 block
+ *              (f32: row-major; bf16 / fp8 / int8: fragment-major, see dwdp_pack_weights)
+ *              fp8: S13 [2I/128, H/128] and S2 [H/128, I/128] fp32 block
  *              scales, one per 128x128 block of W13 / W2 ([out, in] blocks)
+ *              int8: S13 [2I] and S2 [H] fp32 scales, one per row (output channel)
+ *              of W13 / W2, 16-byte aligned
  *   x_perm     [rows, H]         rows = T*k + shared*T: routed rows ordered by
  *                                expert and, inside an expert, by t*k+j; then
  *                                the T shared-expert rows in token order
@@ -75,7 +77,8 @@ typedef enum {
 typedef enum {
     DWDP_F32 = 0,               /* IEEE binary32 */
     DWDP_BF16 = 1,              /* bfloat16 */
-    DWDP_FP8_E4M3 = 2           /* OCP FP8 E4M3 ("FN": no infinities, 448 max), fp32 scales */
+    DWDP_FP8_E4M3 = 2,          /* OCP FP8 E4M3 ("FN": no infinities, 448 max), fp32 scales */
+    DWDP_INT8 = 3               /* signed 8-bit codes, one fp32 scale per token and per weight channel */
 } dwdp_dtype;
 
 typedef enum {
@@ -93,7 +96,7 @@ typedef enum {
 
 /* One entry of the per-expert pointer table (the split-weight "TensorList",
  * paper summary §4.2): where group g's weights live.  s13/s2 are NULL unless
- * the weights are fp8.  Any entry may point into any buffer; two entries may
+ * the weights are fp8 or int8.  Any entry may point into any buffer; two entries may
  * point at the same weights (redundant placement, §2). */
 typedef struct {
     const void* w13;
@@ -180,14 +183,20 @@ int dwdp_quantize_tokens_fp8(const void* x, int64_t T, int H, void* q, float* q_
  *     codes + 128x128 block scales; products accumulated in fp32 per 128-wide K
  *     block and scaled by (row scale * block scale); A quantised per row and
  *     128-column group like x; y_perm bf16.
+ *   w_dtype INT8: x_perm codes + x_perm_scale [rows] (see dwdp_quantize_int8), weights
+ *     codes + channel scales; products summed exactly in 32-bit integers over all of K
+ *     and scaled by (row scale * channel scale); A is fp32, then quantised by row over
+ *     all I columns like x; y_perm bf16.  A token whose scale is NaN (one with an
+ *     infinity or a NaN) gives rows of NaN, and so does a row whose A holds one.
  *   rows must equal offsets[n_groups] (not checked on the device).  H % 256 == 0,
- *   I % 128 == 0 (BF16/FP8; FP8 also H, I <= 8192); H % 64 == 0, I % 32 == 0
- *   (F32).  Other shapes return DWDP_ERR_INVALID_ARG.  offsets is read on the
+ *   I % 128 == 0 (BF16/FP8/INT8; FP8 also H, I <= 8192, INT8 H, I <= 65536);
+ *   H % 64 == 0, I % 32 == 0 (F32).  Other shapes return DWDP_ERR_INVALID_ARG.  offsets is read on the
  *   device only; no host synchronisation happens.
  *   ws: dwdp_workspace_bytes(DWDP_OP_GROUPED_FFN, ...) bytes.  After GEMM1 it
  *     begins with A [rows, I] row-major in the activation type (fp32, bf16, or
- *     E4M3 codes), followed for FP8 at the next 256-byte boundary by A's scales
- *     [rows, I/128] fp32; the tile schedule sits after them. */
+ *     E4M3 or int8 codes), followed for FP8 at the next 256-byte boundary by A's scales
+ *     [rows, I/128] fp32, for INT8 by A's scales [rows] fp32; the tile schedule sits
+ *     after them. */
 int dwdp_moe_grouped_ffn(const dwdp_expert_ptrs* table, int n_groups, const int32_t* offsets,
                          const void* x_perm, const float* x_perm_scale, int64_t rows, int H, int I,
                          int w_dtype, void* y_perm, void* ws, size_t ws_bytes, void* stream);
@@ -205,7 +214,7 @@ int dwdp_moe_grouped_ffn_stage(int stage, const dwdp_expert_ptrs* table, int n_g
  * x[perm_src[r]] (out-of-range indices clamp to [0, T)), which spares the row
  * gather of dwdp_permute and its x_perm round trip through HBM.  x [T,H] holds the
  * tokens (F32 / BF16 as w_dtype; for FP8 the codes of dwdp_quantize_tokens_fp8
- * with x_scale [T,H/128]).  Everything else -- stage, table, offsets, rows,
+ * with x_scale [T,H/128], for INT8 those of dwdp_quantize_int8 with x_scale [T]).  Everything else -- stage, table, offsets, rows,
  * workspace, outputs -- is as in dwdp_moe_grouped_ffn_stage, and the results
  * are bitwise those of the x_perm path. */
 int dwdp_moe_grouped_ffn_tokens(int stage, const dwdp_expert_ptrs* table, int n_groups, const int32_t* offsets,
@@ -265,7 +274,7 @@ int dwdp_prefetch_plan(const dwdp_copy_src* srcs, int n_src, size_t chunk_bytes,
 
 /* Host only: fill a host pointer table from a placement.  Group g's record
  * starts at buffers[buf_of[g]] + slot_of[g] * record_bytes, laid out as
- * [W13 | W2 | S13 | S2] with every part 256-byte aligned (S13/S2 for fp8 only).
+ * [W13 | W2 | S13 | S2] with every part 256-byte aligned (S13/S2 for fp8 and int8 only).
  * The caller uploads `out` (n_groups entries) to device memory. */
 int dwdp_fill_expert_table(void* const* buffers, int n_buffers, const int32_t* buf_of,
                            const int32_t* slot_of, int n_groups, int H, int I, int w_dtype,
@@ -278,12 +287,14 @@ size_t dwdp_expert_record_bytes(int H, int I, int w_dtype);
 int dwdp_expert_record_offsets(int H, int I, int w_dtype, size_t* off_w2, size_t* off_s13,
                                size_t* off_s2);
 
-/* Re-lay a weight matrix w [N, K] (bf16, or fp8 E4M3 codes) into the fragment-major layout the
+/* Re-lay a weight matrix w [N, K] (bf16, fp8 E4M3 codes or int8 codes) into the fragment-major layout the
  * grouped FFN reads (out: N*K elements, same size, must not alias w).  bf16 (K % 64 == 0): the
  * 32 x 16 block (nb, kb) of W is 1 KB at byte (nb*K/16 + kb)*1024, lane l holding row 32nb + l%32,
  * columns 16kb + 8(l/32) .. +7.  fp8 (K % 128 == 0): the 32 x 64 block (nb, kb) is 2 KB at byte
  * (nb*K/64 + kb)*2048; lane l holds row 32nb + l%32, columns 64kb + 32(l/32) .. +31, split in two
- * 16-byte halves at +h*1024 + 16l.  N % 32 == 0.  This is the layout of one MFMA operand per
+ * 16-byte halves at +h*1024 + 16l.  int8 (K % 128 == 0): the 32 x 32 block (nb, kb) is 1 KB at byte
+ * (nb*K/32 + kb)*1024, lane l holding row 32nb + l%32, columns 32kb + 16(l/32) .. +15.
+ * N % 32 == 0.  This is the layout of one MFMA operand per
  * 1-2 KB, so every weight load of the GEMM is a contiguous lane-ordered 1 KB read. */
 int dwdp_pack_weights(const void* w, int64_t N, int64_t K, int dtype, void* out, void* stream);
 

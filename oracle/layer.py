@@ -94,3 +94,17 @@ def combine(y_perm, inv_perm, topk_w, shared):
             z[t] += y[T * k + t]
             mag[t] += np.abs(y[T * k + t])
     return z, mag
+
+
+def branch(u, residual=None, norm=None, eps=0.0, gate=None, token_gate=None, scale=1.0, residual_scale=1.0):
+    """What a layer makes of its block's output u [T,H] before the next norm:
+    residual_scale * residual + scale * token_gate * gate * (u / sqrt(mean(u^2) + eps) * norm)."""
+    n = np.asarray(u, np.float64)
+    if norm is not None:
+        n = n / np.sqrt((n * n).mean(1, keepdims=True) + eps) * np.asarray(norm, np.float64)
+    n = n * scale
+    if gate is not None:
+        n = n * np.asarray(gate, np.float64)
+    if token_gate is not None:
+        n = n * np.asarray(token_gate, np.float64)[:, None]
+    return n if residual is None else n + residual_scale * np.asarray(residual, np.float64)

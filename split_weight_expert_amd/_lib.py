@@ -13,7 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("DWDP_LIBRARY") or os.path.join(HERE, "lib", "libdwdp.so")
 
 DWDP_OK, DWDP_ERR_INVALID_ARG, DWDP_ERR_UNSUPPORTED, DWDP_ERR_WORKSPACE, DWDP_ERR_HIP = range(5)
-F32, BF16, FP8_E4M3 = 0, 1, 2
+F32, BF16, FP8_E4M3, INT8 = 0, 1, 2, 3
 OP_PERMUTE, OP_GROUPED_FFN = 0, 1
 COPY_HIPMEMCPY, COPY_KERNEL, COPY_SDMA = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
@@ -43,6 +43,12 @@ class GateArgs(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("k", ctypes.c_int32), ("n_groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("renormalize", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class BranchArgs(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("norm_dtype", ctypes.c_int32),
+                ("gate_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("scale", ctypes.c_float),
+                ("residual_scale", ctypes.c_float)]
 
 
 class DwdpError(RuntimeError):
@@ -93,6 +99,14 @@ LAYER_SIGNATURES = {
     "dwdp_add_rmsnorm": (_i32, [_vp, _vp, _i32, _vp, _i32, _f32, _i64, _i32, _vp, _vp, _vp, _vp, _vp]),
     "dwdp_combine_add_rmsnorm": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _f32, _vp, _vp,
                                         _vp, _vp, _vp]),
+    "dwdp_branch_add_rmsnorm": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _f32, _i64, _i32, _vp, _vp, _vp, _i32, _vp,
+                                       _vp]),
+    "dwdp_combine_branch_add_rmsnorm": (_i32, [_vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _i32,
+                                               _f32, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "dwdp_quantize_int8": (_i32, [_vp, _i32, _i64, _i32, _vp, _vp, _vp]),
+    "dwdp_balance_loss": (_i32, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dwdp_balance_loss_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "dwdp_gate_backward": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None

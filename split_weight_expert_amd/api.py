@@ -12,9 +12,10 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import BF16, COPY_HIPMEMCPY, COPY_KERNEL, COPY_SDMA, F32, FP8_E4M3, OP_GROUPED_FFN, OP_PERMUTE  # noqa: F401
+from ._lib import (BF16, COPY_HIPMEMCPY, COPY_KERNEL, COPY_SDMA, F32, FP8_E4M3, INT8, OP_GROUPED_FFN,  # noqa: F401
+                   OP_PERMUTE)
 
-_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8_E4M3}
+_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8_E4M3, torch.int8: INT8}
 
 
 def _ptr(t):
@@ -182,7 +183,7 @@ def quantize_weight_fp8(w, q, s, stream=None):
 
 
 def pack_weights(w, out, dtype_code_, stream=None):
-    """Re-lay a weight matrix w [N, K] (bf16, or uint8 E4M3 codes) into the fragment-major layout in out."""
+    """Re-lay a weight matrix w [N, K] (bf16, uint8 E4M3 codes or int8 codes) into the fragment-major layout in out."""
     N, K = w.shape
     _lib.check(_lib.load().dwdp_pack_weights(_ptr(w), N, K, dtype_code_, _ptr(out), _stream(stream)))
 
@@ -331,6 +332,135 @@ def combine_add_rmsnorm(y_perm, inv_perm, topk_w, shared, residual, weight, eps,
     pr, pw, wd, ps, py, pq, pqs = _norm_outputs(T, H, y_perm.dtype, dev, residual, weight, sum_out, y, q, q_scale)
     _lib.check(_lib.load().dwdp_combine_add_rmsnorm(px, pi, pt, T, k, shared, H, _DT[y_perm.dtype], pr, pw, wd, eps, ps,
                                                     py, pq, pqs, _raw_stream(stream, dev)))
+
+
+_CODES = (torch.uint8, torch.int8)
+
+
+@dataclass(frozen=True, eq=False)
+class Branch:
+    """What a layer makes of its block's output before the residual addition (dwdp_branch):
+    residual_scale * residual + scale * token_gate * gate * (output / rms(output) * norm), with norm and gate [H]
+    tensors or None; the token gate [T] belongs to a batch and is given to the calls."""
+    norm: torch.Tensor | None = None
+    eps: float = 1e-6
+    gate: torch.Tensor | None = None
+    scale: float = 1.0
+    residual_scale: float = 1.0
+
+
+def _branch_args(branch, token_gate, T, H, dev):
+    """The C form of a branch and the token gate's address."""
+    if branch is None:
+        c = None
+    else:
+        pn, pg = _check("branch.norm", branch.norm, (H,), _ACT, dev), _check("branch.gate", branch.gate, (H,), _ACT, dev)
+        c = _lib.BranchArgs(pn, pg, F32 if pn is None else _DT[branch.norm.dtype], F32 if pg is None else
+                            _DT[branch.gate.dtype], branch.eps, branch.scale, branch.residual_scale)
+    return None if c is None else ctypes.byref(c), _check("token_gate", token_gate, (T,), _F32, dev)
+
+
+def _branch_outputs(T, H, act, dev, residual, weight, sum_out, y, q, q_scale):
+    act = (act,)
+    int8 = q is not None and q.dtype == torch.int8
+    return (_check("residual", residual, (T, H), act, dev), _check("weight", weight, (H,), _ACT, dev),
+            F32 if weight is None else _DT[weight.dtype], _check("sum_out", sum_out, (T, H), act, dev),
+            _check("y", y, (T, H), act, dev), _check("q", q, (T, H), _CODES, dev), INT8 if int8 else FP8_E4M3,
+            _check("q_scale", q_scale, (T,) if int8 else (T, H // 128), _F32, dev))
+
+
+def branch_add_rmsnorm(x, residual, branch, weight, eps, sum_out=None, y=None, q=None, q_scale=None, token_gate=None,
+                       stream=None):
+    """z = the branch's sum of residual and x; sum_out = z, y = z / rms(z) * weight, (q, q_scale) = y's codes: E4M3 with
+    1x128 scales (uint8 q) or int8 with a scale per token (int8 q)."""
+    T, H = _matrix("x", x)
+    dev = _gpu_index("x", x)
+    px = _check("x", x, (T, H), _ACT, dev)
+    pb, ptg = _branch_args(branch, token_gate, T, H, dev)
+    pr, pw, wd, ps, py, pq, qd, pqs = _branch_outputs(T, H, x.dtype, dev, residual, weight, sum_out, y, q, q_scale)
+    _lib.check(_lib.load().dwdp_branch_add_rmsnorm(px, pr, _DT[x.dtype], pb, ptg, pw, wd, eps, T, H, ps, py, pq, qd, pqs,
+                                                   _raw_stream(stream, dev)))
+
+
+def combine_branch_add_rmsnorm(y_perm, inv_perm, topk_w, shared, residual, branch, weight, eps, sum_out=None, y=None,
+                               q=None, q_scale=None, token_gate=None, stream=None):
+    """The layer boundary with a branch: z = the branch's sum of residual and combine(y_perm); outputs as in
+    branch_add_rmsnorm (weight None: sum_out alone)."""
+    T, k = _matrix("inv_perm", inv_perm)
+    H = _matrix("y_perm", y_perm)[1]
+    dev = _gpu_index("y_perm", y_perm)
+    px = _check("y_perm", y_perm, (T * (k + shared), H), _ACT, dev)
+    pi = _check("inv_perm", inv_perm, (T, k), _I32, dev)
+    pt = _check("topk_w", topk_w, (T, k), _F32, dev)
+    pb, ptg = _branch_args(branch, token_gate, T, H, dev)
+    pr, pw, wd, ps, py, pq, qd, pqs = _branch_outputs(T, H, y_perm.dtype, dev, residual, weight, sum_out, y, q, q_scale)
+    _lib.check(_lib.load().dwdp_combine_branch_add_rmsnorm(px, pi, pt, T, k, shared, H, _DT[y_perm.dtype], pr, pb, ptg, pw,
+                                                           wd, eps, ps, py, pq, qd, pqs, _raw_stream(stream, dev)))
+
+
+def _quantize_int8(x, q, scale, stream):
+    rows, cols = _matrix("x", x)
+    dev = _gpu_index("x", x)
+    px = _check("x", x, (rows, cols), _ACT, dev)
+    pq = _check("q", q, (rows, cols), (torch.int8,), dev)
+    ps = _check("scale", scale, (rows,), _F32, dev)
+    _lib.check(_lib.load().dwdp_quantize_int8(px, _DT[x.dtype], rows, cols, pq, ps, _raw_stream(stream, dev)))
+
+
+def quantize_tokens_int8(x, q, q_scale, stream=None):
+    """Tokens x [T, H] (bf16 or fp32) -> int8 codes q [T, H] and a scale per token q_scale [T]."""
+    _quantize_int8(x, q, q_scale, stream)
+
+
+def quantize_weight_int8(w, q, s, stream=None):
+    """A weight matrix w [out, in] (fp32 or bf16) -> int8 codes q [out, in] and a scale per output channel s [out]."""
+    _quantize_int8(w, q, s, stream)
+
+
+def balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    """Bytes of balance_loss's workspace; a larger T, E or S needs no less."""
+    return int(_lib.load().dwdp_balance_loss_workspace_bytes(T, E, S))
+
+
+def balance_loss(logits, topk_idx, gate, counts, probs, balance, z=None, ws=None, seq_offsets=None, stream=None):
+    """How evenly the sequences [seq_offsets[s], seq_offsets[s + 1]) (None: one of all tokens) load the experts: counts
+    [S, E] int32, mean probabilities probs [S, E], balance loss [S] and z loss [S].  Of the gate its score and k count."""
+    T, E = _matrix("logits", logits)
+    S = _matrix("counts", counts)[0]
+    dev = _gpu_index("logits", logits)
+    pl = _check("logits", logits, (T, E), _F32, dev)
+    pi = _check("topk_idx", topk_idx, (T, gate.k), _I32, dev)
+    pc = _check("counts", counts, (S, E), _I32, dev)
+    pp = _check("probs", probs, (S, E), _F32, dev)
+    pb = _check("balance", balance, (S,), _F32, dev)
+    pz = _check("z", z, (S,), _F32, dev)
+    po = _check("seq_offsets", seq_offsets, (S + 1,), _I32, dev)
+    pws, nws = None, 0
+    if ws is not None:
+        nws = ws.numel() * ws.element_size()
+        pws = _check("ws", ws, ws.shape, (ws.dtype,), dev)
+    _lib.check(_lib.load().dwdp_balance_loss(pl, pi, T, E, gate.k, _SCORES[gate.score], po, S, pc, pp, pb, pz, pws, nws,
+                                             _raw_stream(stream, dev)))
+
+
+def gate_backward(logits, topk_idx, gate, d_logits, d_w=None, counts=None, d_balance=None, d_z=None, seq_offsets=None,
+                  stream=None):
+    """The logits' gradient d_logits [T, E] of the gate's weights (d_w [T, k]) and of balance_loss's two losses (d_balance
+    and d_z [S], with its counts [S, E])."""
+    T, E = _matrix("logits", logits)
+    S = next((t.shape[0] for t in (counts, d_balance, d_z) if t is not None), 1 if seq_offsets is None else
+             seq_offsets.shape[0] - 1)
+    dev = _gpu_index("logits", logits)
+    pl = _check("logits", logits, (T, E), _F32, dev)
+    pi = _check("topk_idx", topk_idx, (T, gate.k), _I32, dev)
+    pd = _check("d_logits", d_logits, (T, E), _F32, dev)
+    pw = _check("d_w", d_w, (T, gate.k), _F32, dev)
+    pc = _check("counts", counts, (S, E), _I32, dev)
+    pb = _check("d_balance", d_balance, (S,), _F32, dev)
+    pz = _check("d_z", d_z, (S,), _F32, dev)
+    po = _check("seq_offsets", seq_offsets, (S + 1,), _I32, dev)
+    _lib.check(_lib.load().dwdp_gate_backward(pl, pi, T, E, ctypes.byref(gate._c), pw, po, S, pc, pb, pz, pd,
+                                              _raw_stream(stream, dev)))
 
 
 # ------------------------------------------------------------------ diagnostics (not steps of the block)

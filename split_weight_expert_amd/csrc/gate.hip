@@ -6,6 +6,7 @@
 
 #include "../../include/dwdp_layer.h"
 #include "common.h"
+#include "gate.h"
 #include "internal.h"
 #include "router.h"
 
@@ -656,26 +657,6 @@ bool aligned4(const void* a, const void* b, const void* c, const void* d, const 
     return type_aligned(a, 4) && type_aligned(b, 4) && type_aligned(c, 4) && type_aligned(d, 4) && type_aligned(e, 4);
 }
 
-int check_gate(const char* fn, const dwdp_gate* g, int E) {
-    auto bad = [&](const char* what) { return fail(DWDP_ERR_INVALID_ARG, std::string(fn) + ": " + what); };
-    if (g == nullptr) return bad("gate is NULL");
-    if (E < 1 || E > kMaxE) return bad("E must be in [1, 1024]");
-    if (g->score != DWDP_SCORE_SOFTMAX && g->score != DWDP_SCORE_SIGMOID)
-        return bad("score must be DWDP_SCORE_SOFTMAX or DWDP_SCORE_SIGMOID");
-    if (g->k < 1 || g->k > E || g->k > kMaxK) return bad("k must be in [1, min(E, 32)]");
-    if (g->n_groups < 1 || g->n_groups > E || E % g->n_groups != 0)
-        return bad("n_groups must divide E");
-    if (g->topk_groups < 1 || g->topk_groups > g->n_groups)
-        return bad("topk_groups must be in [1, n_groups]");
-    if (g->k > g->topk_groups * (E / g->n_groups))
-        return bad("k must be at most the experts of topk_groups groups");
-    if (g->group_top != 1 && g->group_top != 2) return bad("group_top must be 1 or 2");
-    if (g->renormalize != 0 && g->renormalize != 1)
-        return bad("renormalize must be 0 or 1");
-    if (!std::isfinite(g->scale)) return bad("scale must be finite");
-    return DWDP_OK;
-}
-
 GateArgs gate_args(const float* logits, const float* balance, int64_t T, int E, const dwdp_gate& g, int32_t* idx,
                    float* w) {
     GateArgs a{};
@@ -773,6 +754,27 @@ int launch_gate(GateArgs a, hipStream_t st) {
 }
 
 }  // namespace
+
+int check_gate(const char* fn, const dwdp_gate* g, int E) {
+    auto bad = [&](const char* what) { return fail(DWDP_ERR_INVALID_ARG, std::string(fn) + ": " + what); };
+    if (g == nullptr) return bad("gate is NULL");
+    if (E < 1 || E > kMaxE) return bad("E must be in [1, 1024]");
+    if (g->score != DWDP_SCORE_SOFTMAX && g->score != DWDP_SCORE_SIGMOID)
+        return bad("score must be DWDP_SCORE_SOFTMAX or DWDP_SCORE_SIGMOID");
+    if (g->k < 1 || g->k > E || g->k > kMaxK) return bad("k must be in [1, min(E, 32)]");
+    if (g->n_groups < 1 || g->n_groups > E || E % g->n_groups != 0)
+        return bad("n_groups must divide E");
+    if (g->topk_groups < 1 || g->topk_groups > g->n_groups)
+        return bad("topk_groups must be in [1, n_groups]");
+    if (g->k > g->topk_groups * (E / g->n_groups))
+        return bad("k must be at most the experts of topk_groups groups");
+    if (g->group_top != 1 && g->group_top != 2) return bad("group_top must be 1 or 2");
+    if (g->renormalize != 0 && g->renormalize != 1)
+        return bad("renormalize must be 0 or 1");
+    if (!std::isfinite(g->scale)) return bad("scale must be finite");
+    return DWDP_OK;
+}
+
 }  // namespace dwdp
 
 using namespace dwdp;

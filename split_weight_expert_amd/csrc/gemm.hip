@@ -22,6 +22,10 @@
 //     (and for fp8 the re-quantisation of A) happens in the epilogue.
 //     GEMM1 reads its activation rows either from the permuted rows or from
 //     the token rows through perm_src.
+//   * int8 (the same kernel): a byte for byte copy of the bf16 path up to its
+//     MFMA, v_mfma_i32_32x32x32_i8, whose 16-byte operands hold twice the K
+//     columns; the sums are exact 32-bit integers and meet their row and
+//     channel scales in the epilogue.
 //   * f32 (small shapes only): LDS-tiled FMA kernel with the same schedule.
 //   * Router (bf16): router_dma_kernel (up to 512 tiles: operands by DMA into
 //     a four-slot LDS ring) or router_mfma_kernel (two-stage, register-staged).
@@ -65,10 +69,14 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 enum Kind { kGemm1 = 0, kGemm2 = 1, kRouter = 2 };
+enum Prec { kBf16 = 0, kFp8 = 1, kInt8 = 2 };      // operands of gemm_frag_kernel
 
 struct MTile {
     int32_t g;    // group
@@ -80,7 +88,7 @@ static_assert(sizeof(MTile) == kMTileBytes, "the workspace layout sizes the m-ti
 
 struct GemmParams {
     const uint8_t* a;               // activation rows [rows, K]
-    const float* a_scale;           // fp8: [a_nrows, K/128]
+    const float* a_scale;           // fp8: [a_nrows, K/128]; int8: [a_nrows]
     const int32_t* a_rows;          // GEMM1: activation row of permuted row r (token mode), or null
     int64_t a_nrows;                // rows of a
     const dwdp_expert_ptrs* table;  // GEMM1 / GEMM2: per-group weights
@@ -699,10 +707,13 @@ __global__ __launch_bounds__(256) void router_dma_kernel(GemmParams p) {
 // MWV (compile-time: the loop body is straight-line code; only the LDS ring is waited on, and only
 // here, with vmcnt).  Every wave loads its share of the MA blocks' rows whatever its MWV, and a wave
 // with MWV == 0 only loads and keeps the barriers.
-template <int BM, int ROWB, int MA, int MWV, int KIND, bool FP8, int WPOL>
+template <int BM, int ROWB, int MA, int MWV, int KIND, int PREC, int WPOL>
 __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c, uint8_t* smem,
                                           const float* s_bscale) {
+    constexpr bool FP8 = PREC == kFp8, INT8 = PREC == kInt8;
     using C = FragCfg<BM, ROWB, FP8>;
+    using Acc = std::conditional_t<INT8, i32x16, f32x16>;
+    using Operand = std::conditional_t<INT8, i32x4, bf16x8>;   // of one MFMA (bf16, int8)
     constexpr int NS = C::NS, P = C::P, NJ = C::NJ, CH = C::CH, BF = C::BF, STAGE = C::STAGE;
     constexpr int BI = C::BI, BIW = C::BIW, ABYTES = C::ABYTES, BBYTES = C::BBYTES;
     constexpr int RPI = C::RPI, NW = C::NW, MIW = C::MIW;
@@ -721,7 +732,7 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
     const int l32 = lane & 31, hi = lane >> 5;
     const Tile& t = c.t;
     const int KT = c.KT;
-    const size_t lda = (size_t)p.K * (FP8 ? 1 : 2);
+    const size_t lda = (size_t)p.K * (PREC == kBf16 ? 2 : 1);
 
     // fp8: this wave's RW rows of the step's row scales (lanes RW.. idle)
     [[maybe_unused]] const float* gs = nullptr;
@@ -743,13 +754,13 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
         lb[q] = ABYTES + (cg * BI + idx) * 1024;
     }
 
-    f32x16 acc[MW][NJ];
+    Acc acc[MW][NJ];
 #pragma unroll
     for (int i = 0; i < MW; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
     [[maybe_unused]] auto scale_dma = [&](int kt, uint8_t* st) {
         dma4(reinterpret_cast<const uint8_t*>(gs + kt * ROWB / kFp8Group), st + ABYTES + BBYTES + wave * C::SSTRIDE * 4);
@@ -940,12 +951,12 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
     };
 
     if constexpr (!FP8) {
-        // bf16: fragments of the next sub-step are read from LDS while the MFMAs of the current one
+        // bf16, int8: fragments of the next sub-step are read from LDS while the MFMAs of the current one
         // run; the last sub-step of a step first crosses the barrier into the next step's slot.
         constexpr int S = ROWB / 32;
         struct Frags {
-            bf16x8 a[MW];
-            bf16x8 b[NJ];
+            Operand a[MW];
+            Operand b[NJ];
         };
         Frags F[2];
         auto load = [&](Frags& f, int buf, int sub) {
@@ -953,17 +964,19 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
             const uint8_t* A = smem + buf * STAGE;
             const uint8_t* B = A + ABYTES;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) f.b[j] = __builtin_bit_cast(bf16x8, b_frag(B, j, sub));
+            for (int j = 0; j < NJ; ++j) f.b[j] = __builtin_bit_cast(Operand, b_frag(B, j, sub));
 #pragma unroll
-            for (int i = 0; i < MW; ++i) f.a[i] = __builtin_bit_cast(bf16x8, a_frag(A, i, sub * 2 + hi));
+            for (int i = 0; i < MW; ++i) f.a[i] = __builtin_bit_cast(Operand, a_frag(A, i, sub * 2 + hi));
         };
         auto mma = [&](const Frags& f) {
             if (!active) return;
 #pragma unroll
             for (int i = 0; i < MW; ++i)
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < NJ; ++j) {
+                    if constexpr (INT8) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+                    else acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+                }
         };
         // End of step kt (ring slot u) into step kt + 1.  Batch kt + 1 + P goes to the slot of step
         // kt - 1, which every wave stopped reading before the previous barrier; issuing it here, just
@@ -1076,8 +1089,51 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
                     for (int r = 0; r < 16; ++r) acc[i][j][r] *= cprev[i][j];
         }
     }
+    // int8: a lane holds one row of every block, and the columns q * 8 + hi * 4 .. +3 of it for q = 0 .. 3.  A
+    // product's scale is its row's times its channel's.
+    [[maybe_unused]] float rscale[MW];
+    [[maybe_unused]] f32x4 cscale[NJ][4];
+    if constexpr (INT8) {
+#pragma unroll
+        for (int i = 0; i < MW; ++i)
+            rscale[i] = p.a_scale[act_row(p, t.row0 + min(rbase + i * 32 + l32, t.nrows - 1))];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                cscale[j][q] = *reinterpret_cast<const f32x4*>(c.wscale + c.nblk[j] * 32 + q * 8 + hi * 4);
+    }
     if constexpr (KIND == kGemm1) {
-        if constexpr (!FP8) {
+        if constexpr (INT8) {
+            // A's fp32 rows go through LDS and leave in 16-byte pieces; quantize_rows_int8 makes its codes, whose
+            // scale is that of a whole row.  (A rounded to bf16 here would halve these bytes, but move a third of
+            // the codes of large values by one.)
+            ordered_barrier();                                   // every wave is done with the ring
+            uint8_t* stg = smem;                                 // [BM][512 B], chunks c at c ^ (row & 31)
+            if (active) {
+#pragma unroll
+                for (int i = 0; i < MW; ++i) {
+                    const int m = rbase + i * 32 + l32;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f32x4 v;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            v[u] = silu_mul((float)acc[i][0][4 * q + u] * rscale[i] * cscale[0][q][u],
+                                            (float)acc[i][1][4 * q + u] * rscale[i] * cscale[1][q][u]);
+                        *reinterpret_cast<f32x4*>(stg + m * 512 + (((cg * 8 + q * 2 + hi) ^ (m & 31)) << 4)) = v;
+                    }
+                }
+            }
+            __syncthreads();
+            float* out = reinterpret_cast<float*>(p.out);
+            for (int q = threadIdx.x; q < BM * 32; q += NW * 64) {
+                const int row = q >> 5, ch = q & 31;
+                if (row < t.nrows)
+                    *reinterpret_cast<u32x4*>(out + (size_t)(t.row0 + row) * p.N + t.nt * 128 + ch * 4) =
+                        *reinterpret_cast<const u32x4*>(stg + row * 512 + ((ch ^ (row & 31)) << 4));
+            }
+        } else if constexpr (!FP8) {
             // Blocks are transposed (lane l32 holds row rbase + 32 i + l32, element r holds A column
             // cg * 32 + (r >> 2) * 8 + hi * 4 + (r & 3)): A's bf16 rows go through LDS and leave in
             // 16-byte pieces.
@@ -1174,8 +1230,14 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t w0 = bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
-                        const uint32_t w1 = bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+                        float v[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            if constexpr (INT8) v[u] = (float)acc[i][j][4 * q + u] * rscale[i] * cscale[j][q][u];
+                            else v[u] = acc[i][j][4 * q + u];
+                        }
+                        const uint32_t w0 = bf16x2(v[0], v[1]);
+                        const uint32_t w1 = bf16x2(v[2], v[3]);
                         const int byte = (cg * 64 + j * 32 + q * 8 + hi * 4) * 2;
                         uint32_t* d = reinterpret_cast<uint32_t*>(stg + m * 512 + (((byte >> 4) ^ (m & 31)) << 4) + (byte & 15));
                         d[0] = w0;
@@ -1198,8 +1260,10 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
     }
 }
 
-template <int BM, int KIND, bool FP8>
-__global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64), 1) void gemm_frag_kernel(GemmParams p) {
+template <int BM, int KIND, int PREC>
+__global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, PREC == kFp8), PREC == kFp8>::NW * 64), 1)
+    void gemm_frag_kernel(GemmParams p) {
+    constexpr bool FP8 = PREC == kFp8;
     constexpr int ROWB = rowb_of(BM, FP8);
     using C = FragCfg<BM, ROWB, FP8>;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::NS * C::STAGE + C::EXTRA];
@@ -1233,7 +1297,8 @@ __global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64), 1) v
     // hosts waves of another kernel (the layer-ahead prefetch copy); alone it makes no difference.
     __builtin_amdgcn_s_setprio(2);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    c.KT = p.K / (FP8 ? ROWB : ROWB / 2);
+    constexpr int EB = PREC == kBf16 ? 2 : 1;                 // bytes of an operand's element
+    c.KT = p.K / (ROWB / EB);
     const uint8_t* wbase;
     if (KIND == kGemm1) {
         wbase = static_cast<const uint8_t*>(p.table[c.t.g].w13);
@@ -1243,7 +1308,7 @@ __global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64), 1) v
         c.wscale = p.table[c.t.g].s2;
     }
     // fragment-major weights: 4 KB per 32-row n-block per 128 bytes of K
-    const size_t nblk_bytes = (size_t)p.K * (FP8 ? 1 : 2) * 32;
+    const size_t nblk_bytes = (size_t)p.K * EB * 32;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int cg = wave & 3;
@@ -1264,16 +1329,16 @@ __global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64), 1) v
         constexpr int WPOL = decltype(pol)::value;
         if constexpr (C::NW == 4) {
             if constexpr (C::MI == 1) {
-                frag_tile<BM, ROWB, 1, 1, KIND, FP8, WPOL>(p, c, smem, s_bscale);
+                frag_tile<BM, ROWB, 1, 1, KIND, PREC, WPOL>(p, c, smem, s_bscale);
             } else if constexpr (C::MI == 2) {
-                if (ma <= 1) frag_tile<BM, ROWB, 1, 1, KIND, FP8, WPOL>(p, c, smem, s_bscale);
-                else frag_tile<BM, ROWB, 2, 2, KIND, FP8, WPOL>(p, c, smem, s_bscale);
+                if (ma <= 1) frag_tile<BM, ROWB, 1, 1, KIND, PREC, WPOL>(p, c, smem, s_bscale);
+                else frag_tile<BM, ROWB, 2, 2, KIND, PREC, WPOL>(p, c, smem, s_bscale);
             } else {
                 static_assert(C::MI == 4, "4-wave tiles hold at most 128 rows");
-                if (ma <= 1) frag_tile<BM, ROWB, 1, 1, KIND, FP8, WPOL>(p, c, smem, s_bscale);
-                else if (ma == 2) frag_tile<BM, ROWB, 2, 2, KIND, FP8, WPOL>(p, c, smem, s_bscale);
-                else if (ma == 3) frag_tile<BM, ROWB, 3, 3, KIND, FP8, WPOL>(p, c, smem, s_bscale);
-                else frag_tile<BM, ROWB, 4, 4, KIND, FP8, WPOL>(p, c, smem, s_bscale);
+                if (ma <= 1) frag_tile<BM, ROWB, 1, 1, KIND, PREC, WPOL>(p, c, smem, s_bscale);
+                else if (ma == 2) frag_tile<BM, ROWB, 2, 2, KIND, PREC, WPOL>(p, c, smem, s_bscale);
+                else if (ma == 3) frag_tile<BM, ROWB, 3, 3, KIND, PREC, WPOL>(p, c, smem, s_bscale);
+                else frag_tile<BM, ROWB, 4, 4, KIND, PREC, WPOL>(p, c, smem, s_bscale);
             }
         } else {
             // two row parts of MIW m-blocks: the first part takes the first active blocks; a part without
@@ -1283,9 +1348,9 @@ __global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64), 1) v
             auto run = [&](auto tag) {
                 constexpr int MA = decltype(tag)::value;
                 constexpr int W0 = MA < MIW ? MA : MIW, W1 = MA > MIW ? MA - MIW : 0;
-                if (rh == 0) frag_tile<BM, ROWB, MA, W0, KIND, FP8, WPOL>(p, c, smem, s_bscale);
-                else if constexpr (W1 > 0) frag_tile<BM, ROWB, MA, W1, KIND, FP8, WPOL>(p, c, smem, s_bscale);
-                else frag_tile<BM, ROWB, MIW, 0, KIND, FP8, WPOL>(p, c, smem, s_bscale);
+                if (rh == 0) frag_tile<BM, ROWB, MA, W0, KIND, PREC, WPOL>(p, c, smem, s_bscale);
+                else if constexpr (W1 > 0) frag_tile<BM, ROWB, MA, W1, KIND, PREC, WPOL>(p, c, smem, s_bscale);
+                else frag_tile<BM, ROWB, MIW, 0, KIND, PREC, WPOL>(p, c, smem, s_bscale);
             };
             if constexpr (MIW == 4) {
                 if (ma <= 1) run(std::integral_constant<int, 1>{});
@@ -1336,6 +1401,7 @@ __global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64), 1) v
 //   fp8 (K % 128 == 0): fragment (nb, kb) = rows 32nb.., columns 64kb..64kb+63, 2 KB: lane l holds
 //     row 32nb + l%32, columns 64kb + 32(l/32) .. +31; bytes h*16..h*16+15 of that slice sit at
 //     byte (nb * K/64 + kb) * 2048 + h * 1024 + l * 16.
+//   int8 (K % 128 == 0): the bytes of a bf16 matrix of half the columns.
 // Both give 4 KB per 32-row block per 128-byte K step, read as four 1 KB lane-ordered loads.
 __global__ __launch_bounds__(256) void pack_kernel(const uint8_t* __restrict__ w, int64_t N, int64_t K, int fp8,
                                                    uint8_t* __restrict__ out) {
@@ -1484,16 +1550,17 @@ void launch_f32(const GemmParams& p, int64_t tiles, hipStream_t st) {
     hipLaunchKernelGGL(gemm_f32_kernel<KIND>, dim3((unsigned)xcd_grid(tiles)), dim3(256), 0, st, p);
 }
 
-template <int BM, int KIND, bool FP8>
+template <int BM, int KIND, int PREC>
 void launch_dma(const GemmParams& p, int64_t tiles, hipStream_t st) {
+    constexpr bool FP8 = PREC == kFp8;
     constexpr int threads = FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64;
-    hipLaunchKernelGGL((gemm_frag_kernel<BM, KIND, FP8>), dim3((unsigned)xcd_grid(tiles)), dim3(threads), 0, st, p);
+    hipLaunchKernelGGL((gemm_frag_kernel<BM, KIND, PREC>), dim3((unsigned)xcd_grid(tiles)), dim3(threads), 0, st, p);
 }
 
 // g2_wide (fp8, 128-row GEMM1 tiles): GEMM2 runs 256-row tiles, whose schedule replaces GEMM1's in the
 // same tables once GEMM1 is done (so a GEMM2-only call builds it too); maxm_wide bounds their m-tiles.
 template <int BM>
-void launch_ffn(bool g1, bool g2, bool fp8_path, bool g2_wide, const int32_t* offsets, int G, const GemmParams& p1,
+int launch_ffn(bool g1, bool g2, int prec, bool g2_wide, const int32_t* offsets, int G, const GemmParams& p1,
                 const GemmParams& p2, MTile* mt_group, MTile* mt_size, int64_t maxm, int64_t maxm_wide,
                 hipStream_t st) {
     if (g1) launch_schedule<BM>(offsets, G, const_cast<int32_t*>(p1.mprefix), mt_group, mt_size, p1.ticket, st);
@@ -1503,26 +1570,35 @@ void launch_ffn(bool g1, bool g2, bool fp8_path, bool g2_wide, const int32_t* of
     constexpr bool fp8_tiles = BM <= 128;
 #endif
     if constexpr (fp8_tiles) {
-        if (fp8_path) {
-            if (g1) launch_dma<BM, kGemm1, true>(p1, maxm * p1.NT, st);
+        if (prec == kFp8) {
+            if (g1) launch_dma<BM, kGemm1, kFp8>(p1, maxm * p1.NT, st);
             if (g2) {
                 if constexpr (BM == 128) {
                     if (g2_wide) {
                         launch_schedule<256>(offsets, G, const_cast<int32_t*>(p2.mprefix), mt_group, mt_size, nullptr,
                                              st);
-                        launch_dma<256, kGemm2, true>(p2, maxm_wide * p2.NT, st);
-                        return;
+                        launch_dma<256, kGemm2, kFp8>(p2, maxm_wide * p2.NT, st);
+                        return DWDP_OK;
                     }
                 }
-                launch_dma<BM, kGemm2, true>(p2, maxm * p2.NT, st);
+                launch_dma<BM, kGemm2, kFp8>(p2, maxm * p2.NT, st);
             }
-            return;
+            return DWDP_OK;
         }
     }
-    {
-        if (g1) launch_dma<BM, kGemm1, false>(p1, maxm * p1.NT, st);
-        if (g2) launch_dma<BM, kGemm2, false>(p2, maxm * p2.NT, st);
+    if (prec == kInt8) {
+        if (g1) {
+            launch_dma<BM, kGemm1, kInt8>(p1, maxm * p1.NT, st);
+            const int rc = quantize_rows_int8(p1.out, DWDP_F32, p2.a_nrows, p1.N, const_cast<uint8_t*>(p2.a),
+                                              const_cast<float*>(p2.a_scale), st);
+            if (rc != DWDP_OK) return rc;
+        }
+        if (g2) launch_dma<BM, kGemm2, kInt8>(p2, maxm * p2.NT, st);
+        return DWDP_OK;
     }
+    if (g1) launch_dma<BM, kGemm1, kBf16>(p1, maxm * p1.NT, st);
+    if (g2) launch_dma<BM, kGemm2, kBf16>(p2, maxm * p2.NT, st);
+    return DWDP_OK;
 }
 
 }  // namespace
@@ -1567,15 +1643,18 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
                 void* y_perm, void* ws, size_t ws_bytes, void* stream) {
     clear_error();
     DWDP_REQUIRE(stage >= 0 && stage <= 2, "stage must be 0, 1 or 2");
-    DWDP_REQUIRE(w_dtype == DWDP_F32 || w_dtype == DWDP_BF16 || w_dtype == DWDP_FP8_E4M3, "unknown w_dtype");
+    DWDP_REQUIRE(w_dtype == DWDP_F32 || w_dtype == DWDP_BF16 || w_dtype == DWDP_FP8_E4M3 || w_dtype == DWDP_INT8,
+                 "unknown w_dtype");
     DWDP_REQUIRE(n_groups >= 1 && n_groups <= (1 << 20), "n_groups out of range");
     DWDP_REQUIRE(rows >= 0 && rows < (int64_t)1 << 31, "rows out of range");
     DWDP_REQUIRE(H > 0 && I > 0, "H and I must be positive");
     if (w_dtype == DWDP_F32) {
         DWDP_REQUIRE(H % 64 == 0 && I % 32 == 0 && H % 16 == 0 && I % 16 == 0, "f32 path needs H % 64 == 0, I % 32 == 0");
     } else {
-        DWDP_REQUIRE(H % 256 == 0 && I % 128 == 0, "bf16/fp8 paths need H % 256 == 0 and I % 128 == 0");
+        DWDP_REQUIRE(H % 256 == 0 && I % 128 == 0, "bf16/fp8/int8 paths need H % 256 == 0 and I % 128 == 0");
         if (w_dtype == DWDP_FP8_E4M3) DWDP_REQUIRE(H <= 8192 && I <= 8192, "fp8 path needs H, I <= 8192");
+        // 2^16 products of two codes of magnitude 128 are 2^30
+        if (w_dtype == DWDP_INT8) DWDP_REQUIRE(H <= 65536 && I <= 65536, "int8 path needs H, I <= 65536");
     }
     if (rows == 0) return DWDP_OK;
     DWDP_REQUIRE(table && offsets && x && ws && (y_perm || stage == 1), "null pointer argument");
@@ -1584,6 +1663,8 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
     DWDP_REQUIRE(x_rows >= 1 && x_rows < ((int64_t)1 << 31), "x_rows out of range");
     if (w_dtype == DWDP_FP8_E4M3)
         DWDP_REQUIRE(x_scale != nullptr && aligned16(x_scale), "fp8 needs the activation scales, 16-byte aligned");
+    if (w_dtype == DWDP_INT8)
+        DWDP_REQUIRE(x_scale != nullptr && type_aligned(x_scale, 4), "int8 needs the activation scales");
     FfnWs L = ffn_ws_layout(rows, n_groups, I, w_dtype);
     if (ws_bytes < L.total)
         return fail(DWDP_ERR_WORKSPACE, "dwdp_moe_grouped_ffn: workspace too small (need " + std::to_string(L.total) + ")");
@@ -1611,7 +1692,7 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
     p1.I = I;
     p1.NT = w_dtype == DWDP_F32 ? I / (kBnF32 / 2) : I / (kBnDma / 2);
     p1.msuper = w_dtype == DWDP_FP8_E4M3 ? DWDP_MSUPER_FP8 : DWDP_MSUPER_BF16;
-    p1.out = base + L.a;
+    p1.out = base + (w_dtype == DWDP_INT8 ? L.a_f32 : L.a);
     p1.out_scale = reinterpret_cast<float*>(base + L.a_scale);
 
     GemmParams p2 = p1;
@@ -1646,18 +1727,22 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
         if (g2) launch_f32<kGemm2>(p2, maxm * p2.NT, st);
     } else {
         const bool fp8 = w_dtype == DWDP_FP8_E4M3;
+        const int prec = fp8 ? kFp8 : w_dtype == DWDP_INT8 ? kInt8 : kBf16;
         // fp8 GEMM2 in 256-row tiles where the groups average 192 rows or more (the bf16 rule): half the
         // weight re-reads of 128-row tiles; GEMM1 stays at 128 rows (its per-block rescale made 256-row
         // tiles slower there)
         const bool g2_wide = DWDP_FP8_GEMM2_BM256 && fp8 && bm == 128 && rows / n_groups >= 192;
         const int64_t maxm_wide = (rows + 255) / 256 + n_groups;
+        int rc;
         if (bm == 256)
-            launch_ffn<256>(g1, g2, fp8, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
+            rc = launch_ffn<256>(g1, g2, prec, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
         else if (bm == 128)
-            launch_ffn<128>(g1, g2, fp8, g2_wide, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm_wide, st);
+            rc = launch_ffn<128>(g1, g2, prec, g2_wide, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm_wide, st);
         else if (bm == 64)
-            launch_ffn<64>(g1, g2, fp8, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
-        else launch_ffn<32>(g1, g2, fp8, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
+            rc = launch_ffn<64>(g1, g2, prec, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
+        else
+            rc = launch_ffn<32>(g1, g2, prec, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
+        if (rc != DWDP_OK) return rc;
     }
     DWDP_LAUNCHED();
     return DWDP_OK;
@@ -1723,7 +1808,8 @@ extern "C" int dwdp_moe_grouped_ffn_tokens_static(int stage, const dwdp_expert_p
                                                   int w_dtype, void* y_perm, void* stream) {
     clear_error();
     DWDP_REQUIRE(rows >= 0 && n_groups >= 1 && I > 0, "bad rows, n_groups or I");
-    DWDP_REQUIRE(w_dtype == DWDP_F32 || w_dtype == DWDP_BF16 || w_dtype == DWDP_FP8_E4M3, "unknown w_dtype");
+    DWDP_REQUIRE(w_dtype == DWDP_F32 || w_dtype == DWDP_BF16 || w_dtype == DWDP_FP8_E4M3 || w_dtype == DWDP_INT8,
+                 "unknown w_dtype");
     const size_t need = ffn_ws_layout(rows, n_groups, I, w_dtype).total;
     if (need > kStaticScratchBytes)
         return fail(DWDP_ERR_WORKSPACE, "dwdp_moe_grouped_ffn_tokens_static: the workspace of " + std::to_string(rows) +
@@ -1788,12 +1874,14 @@ extern "C" int dwdp_diag_tile_trace_read(dwdp_tile_record* out, size_t max_recor
 
 extern "C" int dwdp_pack_weights(const void* w, int64_t N, int64_t K, int dtype, void* out, void* stream) {
     clear_error();
-    DWDP_REQUIRE(dtype == DWDP_BF16 || dtype == DWDP_FP8_E4M3, "dtype must be DWDP_BF16 or DWDP_FP8_E4M3");
+    DWDP_REQUIRE(dtype == DWDP_BF16 || dtype == DWDP_FP8_E4M3 || dtype == DWDP_INT8,
+                 "dtype must be DWDP_BF16, DWDP_FP8_E4M3 or DWDP_INT8");
     DWDP_REQUIRE(N > 0 && K > 0 && N % 32 == 0, "N must be a positive multiple of 32");
-    DWDP_REQUIRE(K % (dtype == DWDP_BF16 ? 64 : 128) == 0, "K must be a multiple of 64 (bf16) or 128 (fp8)");
+    DWDP_REQUIRE(K % (dtype == DWDP_BF16 ? 64 : 128) == 0, "K must be a multiple of 64 (bf16) or 128 (fp8, int8)");
     DWDP_REQUIRE(w && out && w != out, "w and out must be distinct non-null pointers");
     DWDP_REQUIRE(aligned16(w) && aligned16(out), "w and out must be 16-byte aligned");
-    const int64_t chunks = N * K * (dtype == DWDP_BF16 ? 2 : 1) / 16;
+    if (dtype == DWDP_INT8) K /= 2;                           // laid out as bf16 of half the columns
+    const int64_t chunks = N * K * (dtype == DWDP_FP8_E4M3 ? 1 : 2) / 16;
     const int64_t grid = std::min<int64_t>((chunks + 255) / 256, 65536);
     hipLaunchKernelGGL(pack_kernel, dim3((unsigned)grid), dim3(256), 0, as_stream(stream),
                        static_cast<const uint8_t*>(w), N, K, dtype == DWDP_FP8_E4M3 ? 1 : 0, static_cast<uint8_t*>(out));

@@ -23,6 +23,7 @@ size_t elem_bytes(int dtype) {
         case DWDP_F32: return 4;
         case DWDP_BF16: return 2;
         case DWDP_FP8_E4M3: return 1;
+        case DWDP_INT8: return 1;
         default: return 0;
     }
 }
@@ -39,6 +40,9 @@ void record_layout(int H, int I, int w_dtype, size_t* w2, size_t* s13, size_t* s
         o_s13 = end;
         o_s2 = o_s13 + align256(ns13 * 4);
         end = o_s2 + align256(ns2 * 4);
+    } else if (w_dtype == DWDP_INT8) {
+        o_s2 = o_s13 + align256((size_t)2 * I * 4);
+        end = o_s2 + align256((size_t)H * 4);
     }
     *w2 = o_w2;
     *s13 = o_s13;
@@ -55,6 +59,9 @@ FfnWs ffn_ws_layout(int64_t rows, int groups, int I, int dtype) {
     off += align256((size_t)rows * I * ea);
     w.a_scale = off;
     if (dtype == DWDP_FP8_E4M3) off += align256((size_t)rows * (I / kFp8Group) * 4);
+    if (dtype == DWDP_INT8) off += align256((size_t)rows * 4);
+    w.a_f32 = off;
+    if (dtype == DWDP_INT8) off += align256((size_t)rows * I * 4);
     w.pre = off;
     off += align256((size_t)(groups + 1) * 4);
     w.mt = off;
@@ -233,8 +240,9 @@ int dwdp_fill_expert_table(void* const* buffers, int n_buffers, const int32_t* b
         const char* r = base + (size_t)slot_of[g] * rec;
         out[g].w13 = r;
         out[g].w2 = r + o_w2;
-        out[g].s13 = w_dtype == DWDP_FP8_E4M3 ? reinterpret_cast<const float*>(r + o_s13) : nullptr;
-        out[g].s2 = w_dtype == DWDP_FP8_E4M3 ? reinterpret_cast<const float*>(r + o_s2) : nullptr;
+        const bool scaled = w_dtype == DWDP_FP8_E4M3 || w_dtype == DWDP_INT8;
+        out[g].s13 = scaled ? reinterpret_cast<const float*>(r + o_s13) : nullptr;
+        out[g].s2 = scaled ? reinterpret_cast<const float*>(r + o_s2) : nullptr;
     }
     return DWDP_OK;
 }

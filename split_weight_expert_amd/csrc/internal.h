@@ -29,12 +29,13 @@ inline int64_t hist_chunk(int64_t N) {
 }
 inline int64_t hist_chunks(int64_t N) { return (N + hist_chunk(N) - 1) / hist_chunk(N); }
 
-// Grouped-FFN workspace: A [rows, I] in the activation type (+ its fp8 scales [rows, I/128]), the
+// Grouped-FFN workspace: A [rows, I] in the activation type (+ its fp8 scales [rows, I/128], or int8 scales
+// [rows] and the fp32 values [rows, I] that the codes are made of), the
 // m-tile prefix [G+1], two m-tile tables and the two expert-GEMM launches' tile tickets (int32 each),
 // each part 256-byte aligned; the tables are sized for the smallest tile height, so any tile choice
 // fits.
 struct FfnWs {
-    size_t a, a_scale, pre, mt, mt_by_size, tickets, total;
+    size_t a, a_scale, a_f32, pre, mt, mt_by_size, tickets, total;
 };
 FfnWs ffn_ws_layout(int64_t rows, int groups, int I, int dtype);
 
@@ -46,6 +47,9 @@ std::vector<dwdp_chunk> make_plan(const dwdp_copy_src* srcs, int n_src, size_t c
 int check_sources(const dwdp_copy_src* srcs, int n_src, size_t chunk);
 
 size_t permute_ws_bytes(int64_t T, int k, int E);
+// Rows of x [rows, cols] (DWDP_F32 or DWDP_BF16, 16-byte aligned, cols % 8 == 0) as int8 codes q [rows, cols] and one
+// scale per row (int8.hip); the caller has checked its arguments.
+int quantize_rows_int8(const void* x, int dtype, int64_t rows, int cols, void* q, float* scale, void* stream);
 size_t ffn_ws_bytes(int64_t rows, int groups, int H, int I, int dtype);
 
 }  // namespace dwdp

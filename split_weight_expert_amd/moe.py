@@ -11,7 +11,10 @@ gather=True runs the permute's row gather and the x_perm path instead.
 A model's own gate (api.Gate) takes the place of the plain softmax top-k, and
 norm / forward_normed run the block inside a pre-norm residual layer: the
 norm writes the block's input, and the block ends in the residual addition
-and the next layer's norm.
+and the next layer's norm; an api.Branch puts a norm of the block's output, a
+gate and scales before that addition.  balance and gate_backward are the
+router's training side: how evenly a batch loads the experts, as losses, and
+the gradient of the logits.
 Nothing here computes: every step is a libdwdp call.
 """
 from __future__ import annotations
@@ -23,15 +26,20 @@ import torch
 from torch.multiprocessing.reductions import StorageWeakRef
 
 from . import api
-from ._lib import BF16, F32, FP8_E4M3
+from ._lib import BF16, F32, FP8_E4M3, INT8
 
-DTYPES = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3}
-_ACT_TORCH = {F32: torch.float32, BF16: torch.bfloat16, FP8_E4M3: torch.uint8}
+DTYPES = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3, "int8": INT8}
+_ACT_TORCH = {F32: torch.float32, BF16: torch.bfloat16, FP8_E4M3: torch.uint8, INT8: torch.int8}
 
 
 def act_dtype(w_dtype: int) -> torch.dtype:
-    """torch dtype of the tokens / block output (fp8 layers take bf16 tokens)."""
+    """torch dtype of the tokens / block output (fp8 and int8 layers take bf16 tokens)."""
     return torch.float32 if w_dtype == F32 else torch.bfloat16
+
+
+def _on(stream):
+    """The context in which `stream` is the current one (None: as it is)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class ExpertStore:
@@ -56,15 +64,18 @@ class ExpertStore:
         return self.buffers[buf].data_ptr() + slot * self.rec
 
     def views(self, buf: int, slot: int):
-        """(W13, W2, S13, S2) byte regions of one record (S* are None unless fp8).
+        """(W13, W2, S13, S2) byte regions of one record (S* are None unless fp8 or int8).
 
-        f32 weights are row-major; bf16 and fp8 weights are fragment-major (dwdp_pack_weights).
+        f32 weights are row-major; the others are fragment-major (dwdp_pack_weights).
         """
         r = self.record(buf, slot)
         H, I = self.H, self.I
-        eb = {F32: 4, BF16: 2, FP8_E4M3: 1}[self.w_dtype]
+        eb = {F32: 4, BF16: 2, FP8_E4M3: 1, INT8: 1}[self.w_dtype]
         w13 = r[:2 * I * H * eb]
         w2 = r[self.off_w2:self.off_w2 + H * I * eb]
+        if self.w_dtype == INT8:
+            return (w13, w2, r[self.off_s13:self.off_s13 + 2 * I * 4].view(torch.float32),
+                    r[self.off_s2:self.off_s2 + H * 4].view(torch.float32))
         if self.w_dtype != FP8_E4M3:
             return w13, w2, None, None
         s13 = r[self.off_s13:self.off_s13 + (2 * I // 128) * (H // 128) * 4].view(torch.float32).view(2 * I // 128,
@@ -73,7 +84,7 @@ class ExpertStore:
         return w13, w2, s13, s2
 
     def load(self, buf: int, slot: int, wg: torch.Tensor, wu: torch.Tensor, wd: torch.Tensor, stream=None):
-        """Place one expert's weights ([out, in] device tensors; fp32 masters for fp8) into a record."""
+        """Place one expert's weights ([out, in] device tensors; fp32 masters for fp8 and int8) into a record."""
         w13, w2, s13, s2 = self.views(buf, slot)
         H, I = self.H, self.I
         if self.w_dtype == F32:
@@ -83,6 +94,13 @@ class ExpertStore:
         elif self.w_dtype == BF16:
             api.pack_weights(torch.cat([wg, wu], 0).to(torch.bfloat16).contiguous(), w13, BF16, stream)
             api.pack_weights(wd.to(torch.bfloat16).contiguous(), w2, BF16, stream)
+        elif self.w_dtype == INT8:
+            with _on(stream):
+                q13, q2 = (torch.empty(n, m, dtype=torch.int8, device=w13.device) for n, m in ((2 * I, H), (H, I)))
+                c13, c2 = (torch.empty(n, dtype=torch.float32, device=w13.device) for n in (2 * I, H))
+                api.quantize_weight_int8(torch.cat([wg, wu], 0).float().contiguous(), q13, c13)
+                api.quantize_weight_int8(wd.float().contiguous(), q2, c2)
+                self.load_int8(buf, slot, q13, c13, q2, c2)
         else:
             q13 = torch.empty(2 * I, H, dtype=torch.uint8, device=w13.device)
             q2 = torch.empty(H, I, dtype=torch.uint8, device=w13.device)
@@ -90,6 +108,23 @@ class ExpertStore:
             api.quantize_weight_fp8(wd.float().contiguous(), q2, s2, stream)
             api.pack_weights(q13, w13, FP8_E4M3, stream)
             api.pack_weights(q2, w2, FP8_E4M3, stream)
+
+    def load_int8(self, buf: int, slot: int, w13, s13, w2, s2, stream=None):
+        """Place one expert's int8 codes (w13 [2I, H], gate rows before up rows, and w2 [H, I]) and their scales per output
+        channel (s13 [2I], s2 [H]) into a record."""
+        if self.w_dtype != INT8:
+            raise ValueError("the store's weights are not int8")
+        H, I = self.H, self.I
+        for name, t, shape, dt in (("w13", w13, (2 * I, H), torch.int8), ("s13", s13, (2 * I,), torch.float32),
+                                   ("w2", w2, (H, I), torch.int8), ("s2", s2, (H,), torch.float32)):
+            if t.shape != shape or t.dtype != dt or t.device != self.buffers[buf].device:
+                raise ValueError(f"{name} must be a {dt} tensor of the shape {shape} on {self.buffers[buf].device}")
+        r13, r2, c13, c2 = self.views(buf, slot)
+        with _on(stream):
+            api.pack_weights(w13.contiguous(), r13, INT8)
+            api.pack_weights(w2.contiguous(), r2, INT8)
+            c13.copy_(s13)
+            c2.copy_(s2)
 
     def check_placement(self, placement) -> None:
         """Every (buffer, slot) must name a record inside this store: the C ABI cannot check it, since it
@@ -141,14 +176,24 @@ class Normed:
 
 
 @dataclass
+class Balance:
+    """How evenly S sequences load E experts (api.balance_loss)."""
+    counts: torch.Tensor                  # [S, E] int32
+    probs: torch.Tensor                   # [S, E]
+    balance: torch.Tensor                 # [S]
+    z: torch.Tensor                       # [S]
+    seq_offsets: torch.Tensor | None      # [S + 1], or None: one sequence of all tokens
+
+
+@dataclass
 class BlockBuffers:
     logits: torch.Tensor
     idx: torch.Tensor
     w: torch.Tensor
     x_perm: torch.Tensor | None          # gather mode: permuted rows (fp8: codes)
     x_perm_scale: torch.Tensor | None    # gather mode, fp8
-    x_q: torch.Tensor | None             # token mode, fp8: per-token codes [T, H]
-    x_q_scale: torch.Tensor | None       # token mode, fp8: [T, H/128]
+    x_q: torch.Tensor | None             # token mode, fp8 and int8: per-token codes [T, H]
+    x_q_scale: torch.Tensor | None       # token mode, fp8: [T, H/128], int8: [T]
     offsets: torch.Tensor
     perm_src: torch.Tensor
     inv_perm: torch.Tensor
@@ -156,10 +201,10 @@ class BlockBuffers:
     y: torch.Tensor
     ws_perm: torch.Tensor
     ws_ffn: torch.Tensor
-    x_tokens: torch.Tensor | None = None  # token mode: the rows GEMM1 reads (x, or x_q for fp8)
+    x_tokens: torch.Tensor | None = None  # token mode: the rows GEMM1 reads (x, or x_q for fp8 and int8)
     ws_route: torch.Tensor | None = None  # workspace of the gate's router product (None: it needs none)
     x_norm: torch.Tensor | None = None    # normed layers: the block's input, written by the norm before it
-    normed: Normed | None = None          # the normed input in x_norm (and for fp8 x_q), unless forward() replaced it
+    normed: Normed | None = None          # the normed input in x_norm (fp8, int8: and x_q), unless forward() replaced it
 
 
 class MoEBlock:
@@ -171,6 +216,8 @@ class MoEBlock:
                  gate: api.Gate | None = None):
         if gate is not None and gate.k != k:
             raise ValueError(f"the gate chooses {gate.k} experts, the block is for {k}")
+        if gather and dtype == "int8":
+            raise ValueError("int8 layers read token rows: there is no gather mode for them")
         self.H, self.I, self.E, self.k, self.shared, self.gate = H, I, E, k, shared, gate
         self.w_dtype = DTYPES[dtype]
         self.device = device
@@ -183,8 +230,8 @@ class MoEBlock:
         H, I, E, k, S, dev = self.H, self.I, self.E, self.k, self.shared, self.device
         rows = T * k + S * T
         adt = act_dtype(self.w_dtype)
-        xp_dt = torch.uint8 if self.w_dtype == FP8_E4M3 else adt
-        fp8 = self.w_dtype == FP8_E4M3
+        xp_dt = _ACT_TORCH[self.w_dtype]
+        fp8, int8 = self.w_dtype == FP8_E4M3, self.w_dtype == INT8
         g = self.gather
         ws_p = api.workspace_bytes(api.OP_PERMUTE, T, k, E, H, I, self.w_dtype, S)
         ws_f = api.workspace_bytes(api.OP_GROUPED_FFN, T, k, E, H, I, self.w_dtype, S)
@@ -195,8 +242,9 @@ class MoEBlock:
             w=torch.empty(T, k, dtype=torch.float32, device=dev),
             x_perm=torch.empty(rows, H, dtype=xp_dt, device=dev) if g else None,
             x_perm_scale=torch.empty(rows, H // 128, dtype=torch.float32, device=dev) if g and fp8 else None,
-            x_q=torch.empty(T, H, dtype=torch.uint8, device=dev) if fp8 and not g else None,
-            x_q_scale=torch.empty(T, H // 128, dtype=torch.float32, device=dev) if fp8 and not g else None,
+            x_q=torch.empty(T, H, dtype=xp_dt, device=dev) if (fp8 or int8) and not g else None,
+            x_q_scale=torch.empty((T,) if int8 else (T, H // 128), dtype=torch.float32, device=dev)
+            if (fp8 or int8) and not g else None,
             offsets=torch.empty(E + S + 1, dtype=torch.int32, device=dev),
             perm_src=torch.empty(rows, dtype=torch.int32, device=dev),
             inv_perm=torch.empty(T, k, dtype=torch.int32, device=dev),
@@ -219,14 +267,17 @@ class MoEBlock:
         api.route_topk(x, w_router, bias, self.k, b.logits, b.idx, b.w, stream)
 
     def permute(self, x, b: BlockBuffers, stream=None):
-        """Expert permutation; gather mode also writes x_perm, token mode quantises the tokens for fp8."""
-        b.normed = None                       # fp8: the codes below take the normed ones' place
+        """Expert permutation; gather mode also writes x_perm, token mode quantises the tokens for fp8 and int8."""
+        b.normed = None                       # fp8, int8: the codes below take the normed ones' place
         fp8 = self.w_dtype == FP8_E4M3
         api.permute(b.idx, self.E, self.shared, x, self.w_dtype if fp8 else api.dtype_code(x),
                     b.x_perm, b.x_perm_scale, b.offsets, b.perm_src, b.inv_perm, b.ws_perm, stream)
         if not self.gather:
             if fp8:
                 api.quantize_tokens_fp8(x, b.x_q, b.x_q_scale, stream)
+                b.x_tokens = b.x_q
+            elif self.w_dtype == INT8:
+                api.quantize_tokens_int8(x, b.x_q, b.x_q_scale, stream)
                 b.x_tokens = b.x_q
             else:
                 b.x_tokens = x
@@ -254,9 +305,37 @@ class MoEBlock:
         self.combine(b, stream, out)
         return b
 
+    # The router's training side.  Both read the logits and the choice that the last route() left in the buffers.
+
+    def _gate(self) -> api.Gate:
+        return api.Gate(self.k) if self.gate is None else self.gate
+
+    def balance(self, b: BlockBuffers, seq_offsets=None, stream=None) -> Balance:
+        """Per-expert counts, the balance loss and the z loss of the sequences [seq_offsets[s], seq_offsets[s + 1]) of the
+        routed batch (None: one sequence of all its tokens)."""
+        T, E = b.logits.shape
+        S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+        with _on(stream):
+            def empty(*shape, dtype=torch.float32):
+                return torch.empty(*shape, dtype=dtype, device=b.logits.device)
+            r = Balance(empty(S, E, dtype=torch.int32), empty(S, E), empty(S), empty(S), seq_offsets)
+            ws = empty(api.balance_loss_workspace_bytes(T, E, S), dtype=torch.uint8)
+            api.balance_loss(b.logits, b.idx, self._gate(), r.counts, r.probs, r.balance, r.z, ws, seq_offsets)
+        return r
+
+    def gate_backward(self, b: BlockBuffers, d_w=None, balance: Balance | None = None, d_balance=None, d_z=None, out=None,
+                      stream=None) -> torch.Tensor:
+        """Gradient [T, E] of the routed batch's logits, from that of the weights b.w (d_w) and of `balance`'s losses, to
+        `out` if given."""
+        with _on(stream):
+            out = torch.empty_like(b.logits) if out is None else out
+            counts, offsets = (None, None) if balance is None else (balance.counts, balance.seq_offsets)
+            api.gate_backward(b.logits, b.idx, self._gate(), out, d_w, counts, d_balance, d_z, offsets)
+        return out
+
     # A pre-norm layer is h' = h + block(norm(h)).  The norm of a layer's input is written by `norm` (a
     # model's first layer) or by the layer before it (forward_normed's next_weight), into b.x_norm and, for
-    # fp8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.  fp8 layers in gather
+    # fp8 and int8 layers that read token rows, into the codes b.x_q: those layers skip the token quantiser.  fp8 layers in gather
     # mode quantise the rows of b.x_norm as they gather them, as forward() does its tokens: their codes are those of the
     # norm rounded to bf16, the others' of the unrounded norm, so the two modes differ by that rounding.  All batches of
     # one size share these buffers, so forward_normed asks whose norm they hold.
@@ -264,24 +343,37 @@ class MoEBlock:
     def _norm_outputs(self, b: BlockBuffers, stream=None):
         if b.x_norm is None:
             # on the stream that writes it first: the allocator may give memory whose last reader on another is not done
-            with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            with _on(stream):
                 b.x_norm = torch.empty_like(b.y)
         return dict(y=b.x_norm, q=b.x_q, q_scale=b.x_q_scale)
 
-    def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None) -> Normed:
-        """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given).
+    def _plain(self, branch, token_gate) -> bool:
+        """Whether the norms without a branch do: int8 codes come from those with one."""
+        return branch is None and token_gate is None and self.w_dtype != INT8
+
+    def norm(self, x, weight, eps: float, b: BlockBuffers, residual=None, sum_out=None, stream=None,
+             branch: api.Branch | None = None, token_gate=None) -> Normed:
+        """b's input of the next forward_normed: the norm of x (+ residual; the sum goes to sum_out if given).  With a
+        branch x is the output of what ran before this block (e.g. attention), and the branch says how it meets residual.
 
         That forward_normed is called with the normed tensor, which is sum_out if given and else x; or with the handle
         returned here, which it needs after a norm of x + residual whose sum went nowhere."""
         b.normed = None                       # a refused norm is none, whatever was there before
-        api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b, stream))
-        b.normed = Normed(sum_out if sum_out is not None else x if residual is None else None)
+        if self._plain(branch, token_gate):
+            api.add_rmsnorm(x, residual, weight, eps, sum_out=sum_out, stream=stream, **self._norm_outputs(b, stream))
+        else:
+            api.branch_add_rmsnorm(x, residual, branch, weight, eps, sum_out=sum_out, token_gate=token_gate, stream=stream,
+                                   **self._norm_outputs(b, stream))
+        sums = residual is not None or branch is not None or token_gate is not None
+        b.normed = Normed(sum_out if sum_out is not None else None if sums else x)
         return b.normed
 
     def forward_normed(self, h, w_router, bias, table, next_weight=None, eps: float = 1e-6, stream=None, out=None,
-                       balance_bias=None, normed: Normed | None = None) -> BlockBuffers:
+                       balance_bias=None, normed: Normed | None = None, branch: api.Branch | None = None,
+                       token_gate=None) -> BlockBuffers:
         """A layer whose normed input is in the buffers: h + block(b.x_norm) to `out` (b.y if not given; h itself
-        works), and with next_weight that sum's norm to the buffers, the next layer's input.
+        works), and with next_weight that sum's norm to the buffers, the next layer's input.  branch and token_gate [T]:
+        what the layer makes of its block's output before it meets h.
 
         The buffers must hold the norm of h: that of another tensor, or of what h was before torch wrote to it, is
         refused (another batch of the same size may have been normed since).  With `normed`, the handle of the normed
@@ -303,8 +395,13 @@ class MoEBlock:
         self.ffn(table, b, stream)
         out = b.y if out is None else out
         now, b.normed = b.normed, None
-        api.combine_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, next_weight, eps, sum_out=out, stream=stream,
-                                **(self._norm_outputs(b, stream) if next_weight is not None else {}))
+        outputs = self._norm_outputs(b, stream) if next_weight is not None else {}
+        if self._plain(branch, token_gate):
+            api.combine_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, next_weight, eps, sum_out=out, stream=stream,
+                                    **outputs)
+        else:
+            api.combine_branch_add_rmsnorm(b.y_perm, b.inv_perm, b.w, self.shared, h, branch, next_weight, eps, sum_out=out,
+                                           token_gate=token_gate, stream=stream, **outputs)
         if next_weight is not None:
             b.normed = Normed(out)
         elif (not now.shares_memory(out) and out.data_ptr() != h.data_ptr() and
@@ -330,6 +427,7 @@ class LayerWeights:
     balance_bias: torch.Tensor | None = None   # with a gate: steers the choice of experts
     norm: torch.Tensor | None = None           # weight of the RMS norm before the block (None: no norm, no residual)
     norm_eps: float = 1e-6
+    branch: api.Branch | None = None           # with a norm: what the block's output goes through before it meets h
 
 
 class DWDPPipeline:
@@ -348,7 +446,8 @@ class DWDPPipeline:
     resident records and the current slot set -- so nothing is merged.  Only the MoE blocks run here
     (a model without attention): layer l+1's input is layer l's output.  Layers with a norm weight are
     pre-norm residual layers, h_{l+1} = h_l + block_l(norm_l(h_l)): the first norm runs by itself, every
-    other one in the pass that combines the layer before it.
+    other one in the pass that combines the layer before it.  A layer's branch (a norm after the block, a
+    gate, scales) is part of that same pass.
     """
 
     def __init__(self, H: int, I: int, E: int, k: int, shared: int, dtype: str, n_local: int, device="cuda",
@@ -416,6 +515,8 @@ class DWDPPipeline:
         normed = L > 0 and layers[0].norm is not None
         if any((lw.norm is not None) != normed for lw in layers):
             raise ValueError("some layers have a norm and some have none")
+        if not normed and any(lw.branch is not None for lw in layers):
+            raise ValueError("a branch needs a layer with a norm")
         if normed and not chain:
             raise ValueError("layers with norms are a chain")
         T = x.shape[0]
@@ -452,7 +553,7 @@ class DWDPPipeline:
                 b = self.block.forward_normed(x, lw.w_router, lw.bias, self.table(lw, s),
                                               next_weight=None if nxt is None else nxt.norm,
                                               eps=lw.norm_eps if nxt is None else nxt.norm_eps, out=outputs[l],
-                                              balance_bias=lw.balance_bias, normed=handle)
+                                              balance_bias=lw.balance_bias, normed=handle, branch=lw.branch)
                 handle = b.normed
             else:
                 b = self.block.forward(x, lw.w_router, lw.bias, self.table(lw, s), out=outputs[l],
