@@ -18,7 +18,9 @@ namespace {
 
 constexpr int kMaxE = 1024;
 constexpr int kMaxSeqs = 1 << 20;
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;          // of the loss's workgroups
+constexpr int kGradThreads = 256;
+constexpr int64_t kGradWgs = 1024;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 struct BalanceArgs {
@@ -30,8 +32,8 @@ struct BalanceArgs {
     const int32_t* offsets;           // [S+1] or null (one sequence)
     int chunk, n_chunks;
     // loss
-    float* part_p;                    // [n_chunks][E] sums of p
-    int32_t* part_n;                  // [n_chunks][E] counts
+    float* part_p;                    // [n_chunks][E rounded up to 4] sums of p
+    int32_t* part_n;                  // the same, counts
     float* part_z;                    // [n_chunks] sums of logsumexp^2
     int32_t* counts;                  // [S][E]; read by the gradient
     float* probs;
@@ -47,36 +49,47 @@ struct BalanceArgs {
 };
 
 // First token of sequence s, for s in [0, S].
-__device__ __forceinline__ int64_t seq_start(const BalanceArgs& a, int s) {
-    if (a.offsets == nullptr) return s == 0 ? 0 : a.T;
-    const int64_t o = a.offsets[s];
-    return o < 0 ? 0 : o > a.T ? a.T : o;
+__device__ __forceinline__ uint32_t seq_start(const BalanceArgs& a, int s) {
+    if (a.offsets == nullptr) return s == 0 ? 0 : (uint32_t)a.T;
+    return (uint32_t)min(max(a.offsets[s], 0), (int)a.T);
 }
 
 // The gradient covers the tokens of no sequence too: runs 0 .. S+1 are those before the first, the sequences, and
 // those behind the last.
-__device__ __forceinline__ int64_t run_start(const BalanceArgs& a, int r) {
-    return r == 0 ? 0 : r == a.S + 2 ? a.T : seq_start(a, r - 1);
+__device__ __forceinline__ uint32_t run_start(const BalanceArgs& a, int r) {
+    return r == 0 ? 0 : r == a.S + 2 ? (uint32_t)a.T : seq_start(a, r - 1);
 }
 
 template <bool RUNS>
-__device__ __forceinline__ int64_t part_start(const BalanceArgs& a, int s) {
+__device__ __forceinline__ uint32_t part_start(const BalanceArgs& a, int s) {
     return RUNS ? run_start(a, s) : seq_start(a, s);
 }
 
 // The sequence (run) of this workgroup's chunk, and the chunk's tokens [first, last).
 template <bool RUNS>
 __device__ __forceinline__ int find_chunk(const BalanceArgs& a, int64_t* first, int64_t* last) {
+    constexpr int kWg = RUNS ? kGradThreads : kThreads;
     const int c = blockIdx.x, n = RUNS ? a.S + 2 : a.S;
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {                          // the last one that starts at or before chunk c
-        const int mid = (lo + hi + 1) / 2;
-        if (part_start<RUNS>(a, mid) / a.chunk + mid <= c) lo = mid;
-        else hi = mid - 1;
+    const uint32_t chunk = a.chunk;
+    // the last one that starts at or before chunk c: every thread asks for its own, which costs one read's latency, or,
+    // where there are many, one search
+    int lo = 0;
+    if (n <= 4 * kWg) {
+        for (int s = threadIdx.x; s - (int)threadIdx.x < n; s += kWg) {
+            const bool before = s > 0 && s < n && (int)(part_start<RUNS>(a, s) / chunk) + s <= c;
+            lo += __syncthreads_count(before);
+        }
+    } else {
+        int hi = n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if ((int)(part_start<RUNS>(a, mid) / chunk) + mid <= c) lo = mid;
+            else hi = mid - 1;
+        }
     }
-    const int64_t start = part_start<RUNS>(a, lo), end = part_start<RUNS>(a, lo + 1);
-    *first = start + (c - (start / a.chunk + lo)) * (int64_t)a.chunk;
-    *last = min(*first + a.chunk, end);
+    const uint32_t start = part_start<RUNS>(a, lo), end = part_start<RUNS>(a, lo + 1);
+    *first = start + (int64_t)(c - ((int)(start / chunk) + lo)) * chunk;
+    *last = min(*first + chunk, (int64_t)end);
     return lo;
 }
 
@@ -91,6 +104,12 @@ struct TokenProbs {
     float lse;            // logsumexp(l), 0 for a token without a live logit
 };
 
+// Orders the LDS accesses of one wave.
+__device__ __forceinline__ void wave_lds_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A sigmoid's e^l / (1 + e^l) is e^l to fp32's last bit where every logit is below this, and there the sigmoids'
 // shares are a softmax's, whatever underflows.
 constexpr float kTiny = -30.0f;
@@ -103,19 +122,24 @@ __device__ __forceinline__ float row_fmax(float v) {
     return __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
 }
 
+// Every division is by the hardware reciprocal (1 ulp): the exact one's ten instructions were a third of these kernels.
+__device__ __forceinline__ float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
+
+// e^(l - top), where top may be +inf.
 __device__ __forceinline__ float exp_from(float l, float top) { return l == top ? 1.0f : __expf(l - top); }
 
+// -inf gives 0 and 1, +inf 1 and 0.
 __device__ __forceinline__ void sigmoid_of(float l, float* s, float* one_minus_s) {
-    const float e = __expf(-fabsf(l)), r = 1.0f / (1.0f + e);
-    *s = l >= 0.0f ? r : e * r;
-    *one_minus_s = l >= 0.0f ? e * r : r;
+    const float e = __expf(-fabsf(l)), r = rcp(1.0f + e), er = e * r;
+    *s = l >= 0.0f ? r : er;
+    *one_minus_s = l >= 0.0f ? er : r;
 }
 
 template <int PL, int LANES>
 __device__ __forceinline__ void token_probs(const BalanceArgs& a, TokenProbs<PL, LANES>& t) {
-    float top = kNegInf;
+    float top = t.l[0];
 #pragma unroll
-    for (int u = 0; u < PL; ++u) top = fmaxf(top, t.l[u]);
+    for (int u = 1; u < PL; ++u) top = fmaxf(top, t.l[u]);
     top = row_fmax<LANES>(top);
     t.top = top;
     if (top == kNegInf) {
@@ -128,14 +152,40 @@ __device__ __forceinline__ void token_probs(const BalanceArgs& a, TokenProbs<PL,
         return;
     }
     float sum = 0.0f;
+    if (a.sigmoid && top >= 0.0f && top < 80.0f) {
+        // x = e^l does for both: x / (1 + x) and x / sum of x; what underflows is below 2^-126 of the sum
+        float total = 0.0f;
 #pragma unroll
-    for (int u = 0; u < PL; ++u) {
-        t.soft[u] = t.l[u] == kNegInf ? 0.0f : exp_from(t.l[u], top);
-        sum += t.soft[u];
+        for (int u = 0; u < PL; ++u) {
+            const float x = __expf(t.l[u]);
+            t.slope[u] = rcp(1.0f + x);
+            t.p[u] = x * t.slope[u];
+            t.soft[u] = x;
+            sum += x;
+            total += t.p[u];
+        }
+        sum = row_sum<LANES>(sum);
+        t.lse = __logf(sum);
+        t.inv = rcp(sum);
+        const float f = rcp(row_sum<LANES>(total));
+#pragma unroll
+        for (int u = 0; u < PL; ++u) {
+            t.soft[u] *= t.inv;
+            t.p[u] *= f;
+        }
+        t.inv *= __expf(top);
+        return;
+    }
+    if (top < __builtin_huge_valf()) {
+#pragma unroll
+        for (int u = 0; u < PL; ++u) sum += t.soft[u] = __expf(t.l[u] - top);      // 0 for -inf
+    } else {
+#pragma unroll
+        for (int u = 0; u < PL; ++u) sum += t.soft[u] = t.l[u] == top ? 1.0f : 0.0f;
     }
     sum = row_sum<LANES>(sum);
     t.lse = top + __logf(sum);
-    t.inv = 1.0f / sum;
+    t.inv = rcp(sum);
 #pragma unroll
     for (int u = 0; u < PL; ++u) {
         t.soft[u] *= t.inv;
@@ -146,26 +196,35 @@ __device__ __forceinline__ void token_probs(const BalanceArgs& a, TokenProbs<PL,
         float total = 0.0f;
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
-            t.p[u] = 0.0f;
-            if (t.l[u] > kNegInf) sigmoid_of(t.l[u], &t.p[u], &t.slope[u]);
+            sigmoid_of(t.l[u], &t.p[u], &t.slope[u]);
             total += t.p[u];
         }
-        const float f = 1.0f / row_sum<LANES>(total);
+        const float f = rcp(row_sum<LANES>(total));
 #pragma unroll
         for (int u = 0; u < PL; ++u) t.p[u] *= f;
     }
 }
 
+// Reads are issued here and looked at in live_logits: a NaN, and what is behind the last expert, takes no part.
 template <int PL, int LANES>
-__device__ __forceinline__ void load_logits(const BalanceArgs& a, int64_t tok, int lane, float* l) {
+__device__ __forceinline__ void live_logits(const BalanceArgs& a, int lane, float* l) {
 #pragma unroll
-    for (int u = 0; u < PL; ++u) {
-        const int e = lane + LANES * u;
-        const float v = e < a.E ? a.logits[tok * a.E + e] : kNegInf;
-        l[u] = v == v ? v : kNegInf;           // NaN
-    }
+    for (int u = 0; u < PL; ++u) l[u] = lane + LANES * u < a.E ? fmaxf(l[u], kNegInf) : kNegInf;
 }
 
+template <int PL, int LANES>
+__device__ __forceinline__ void load_logits(const BalanceArgs& a, int64_t tok, int lane, float* l) {
+    // the last expert's in the place of those behind it, so that no branch parts the reads
+    const float* row = a.logits + tok * a.E;
+#pragma unroll
+    for (int u = 0; u < PL; ++u) l[u] = row[min(lane + LANES * u, a.E - 1)];
+}
+
+// Bound by latency up to some thousand tokens (an empty kernel takes 2.3 us, two of them and their parts' dependent reads
+// 7 us), and by instructions, not bytes, beyond: sigmoids, 256 experts, 65536 tokens are 67 MB in 28 us.  16384 tokens in
+// four sequences 14.4 us, of which the second launch takes 6.  Before (a wave a token, exact divisions, reads parted by
+// branches) 25.9 us.
+//
 // Sums of one chunk: lanes add their experts' probabilities over the tokens, then the token groups meet in LDS.
 template <int PL, int LANES>
 __global__ __launch_bounds__(kThreads) void balance_chunk_kernel(BalanceArgs a) {
@@ -177,18 +236,27 @@ __global__ __launch_bounds__(kThreads) void balance_chunk_kernel(BalanceArgs a) 
     find_chunk<false>(a, &first, &last);
     if (first >= last) return;
     const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
-    for (int e = tid; e < a.E; e += kThreads) s_n[e] = 0;
+    // the first token's reads are on their way while the counts are cleared; the next one's while one is summed
+    float next[PL], sum[PL], zsum = 0.0f;
+    int e_next = -1;
+    auto fetch = [&](int64_t t) {
+        if (t >= last) return;
+        load_logits<PL, LANES>(a, t, lane, next);
+        if (lane < a.k) e_next = a.idx[t * a.k + lane];
+    };
+    fetch(first + group);
+    for (int e = tid; e < kMaxE; e += kThreads) s_n[e] = 0;
     __syncthreads();
-    for (int64_t i = first * a.k + tid; i < last * a.k; i += kThreads) {
-        const int e = a.idx[i];
-        if (e >= 0 && e < a.E) atomicAdd(&s_n[e], 1);
-    }
-    float sum[PL], zsum = 0.0f;
 #pragma unroll
     for (int u = 0; u < PL; ++u) sum[u] = 0.0f;
     for (int64_t t = first + group; t < last; t += R) {
         TokenProbs<PL, LANES> tp;
-        load_logits<PL, LANES>(a, t, lane, tp.l);
+#pragma unroll
+        for (int u = 0; u < PL; ++u) tp.l[u] = next[u];
+        const int e = e_next;
+        fetch(t + R);
+        live_logits<PL, LANES>(a, lane, tp.l);
+        if (lane < a.k && e >= 0 && e < a.E) atomicAdd(&s_n[e], 1);
         token_probs(a, tp);
 #pragma unroll
         for (int u = 0; u < PL; ++u) sum[u] += tp.p[u];
@@ -198,11 +266,14 @@ __global__ __launch_bounds__(kThreads) void balance_chunk_kernel(BalanceArgs a) 
     for (int u = 0; u < PL; ++u) s_p[group * (LANES * PL) + u * LANES + lane] = sum[u];
     if (lane == 0) s_z[group] = zsum;
     __syncthreads();
-    const int64_t row = (int64_t)blockIdx.x * a.E;
-    for (int e = tid; e < a.E; e += kThreads) {
+    const int E4 = (a.E + 3) & ~3;
+    const int64_t row = (int64_t)blockIdx.x * E4;
+    for (int e = tid; e < E4; e += kThreads) {
         float v = 0.0f;
+        if (e < LANES * PL) {
 #pragma unroll
-        for (int g = 0; g < R; ++g) v += s_p[g * (LANES * PL) + e];
+            for (int g = 0; g < R; ++g) v += s_p[g * (LANES * PL) + e];      // 0 behind the last expert
+        }
         a.part_p[row + e] = v;
         a.part_n[row + e] = s_n[e];
     }
@@ -213,45 +284,57 @@ __global__ __launch_bounds__(kThreads) void balance_chunk_kernel(BalanceArgs a) 
     }
 }
 
-// One sequence: its chunks' rows added in order, `width` experts side by side and 1024 / width rows at a time.
+// One sequence: its chunks' rows added, four experts a thread, `width` threads side by side and 1024 / width rows at a
+// time; the sums of a chunk are fp32, those over chunks fp64.
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a, int width) {
-    __shared__ double s_p[1024];
+    __shared__ double s_p[4 * 1024];
+    __shared__ int s_n[4 * 1024];
     __shared__ float s_b[16];
-    __shared__ int s_n[1024];
-    const int s = blockIdx.x, tid = threadIdx.x, e = tid % width, part = tid / width, parts = 1024 / width;
-    const int64_t start = seq_start(a, s), n = max((int64_t)0, seq_start(a, s + 1) - start);
-    const int c0 = (int)(start / a.chunk) + s, nc = (int)((n + a.chunk - 1) / a.chunk);
-    double p = 0.0;
-    int cnt = 0;
-    if (e < a.E) {
-#pragma unroll 8
+    const int s = blockIdx.x, tid = threadIdx.x, col = tid % width, part = tid / width, parts = 1024 / width;
+    const int E4 = (a.E + 3) & ~3;
+    const uint32_t start = seq_start(a, s), end = seq_start(a, s + 1), n = end > start ? end - start : 0;
+    const int64_t c0 = start / (uint32_t)a.chunk + s;
+    const int nc = (int)((n + a.chunk - 1) / (uint32_t)a.chunk);
+    double p[4] = {0.0, 0.0, 0.0, 0.0};
+    int cnt[4] = {0, 0, 0, 0};
+    if (4 * col < E4) {
+#pragma unroll 4
         for (int c = part; c < nc; c += parts) {
-            p += a.part_p[(int64_t)(c0 + c) * a.E + e];
-            cnt += a.part_n[(int64_t)(c0 + c) * a.E + e];
+            const int64_t i = (c0 + c) * E4 + 4 * col;
+            const float4 v = *reinterpret_cast<const float4*>(a.part_p + i);
+            const int4 m = *reinterpret_cast<const int4*>(a.part_n + i);
+            p[0] += v.x, p[1] += v.y, p[2] += v.z, p[3] += v.w;
+            cnt[0] += m.x, cnt[1] += m.y, cnt[2] += m.z, cnt[3] += m.w;
         }
     }
-    s_p[tid] = p;
-    s_n[tid] = cnt;
-    __syncthreads();
-    float b = 0.0f;
-    if (part == 0 && e < a.E) {
-        for (int i = 1; i < parts; ++i) {
-            p += s_p[i * width + e];
-            cnt += s_n[i * width + e];
-        }
-        const float mean = n > 0 ? (float)(p / (double)n) : 0.0f;
-        a.counts[(int64_t)s * a.E + e] = cnt;
-        a.probs[(int64_t)s * a.E + e] = mean;
-        b = n > 0 ? (float)cnt / (float)n * ((float)a.E / (float)a.k) * mean : 0.0f;
-    }
-    b = row_sum<64>(b);
-    if ((tid & 63) == 0) s_b[tid >> 6] = b;
     float z = 0.0f;
     if (a.z != nullptr && tid < 64) {
         double sum = 0.0;
         for (int c = tid; c < nc; c += 64) sum += a.part_z[c0 + c];
         z = row_sum<64>((float)sum);
     }
+    // [part][4 width]
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        s_p[4 * tid + u] = p[u];
+        s_n[4 * tid + u] = cnt[u];
+    }
+    __syncthreads();
+    float b = 0.0f;
+    if (tid < a.E) {
+        double sum = 0.0;
+        int m = 0;
+        for (int i = 0; i < parts; ++i) {
+            sum += s_p[i * 4 * width + tid];
+            m += s_n[i * 4 * width + tid];
+        }
+        const float mean = n > 0 ? (float)(sum / (double)n) : 0.0f;
+        a.counts[(int64_t)s * a.E + tid] = m;
+        a.probs[(int64_t)s * a.E + tid] = mean;
+        b = n > 0 ? (float)m / (float)n * ((float)a.E / (float)a.k) * mean : 0.0f;
+    }
+    b = row_sum<64>(b);
+    if ((tid & 63) == 0) s_b[tid >> 6] = b;
     __syncthreads();
     if (tid == 0) {
         float v = 0.0f;
@@ -261,11 +344,15 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a, int
     }
 }
 
+// Bound as the loss is: 64 tokens of 256 experts 4.7 us, 16384 15.3 us (50 MB at 3.3 TB/s), 65536 36 us (3.7 TB/s).
+// Before (a workgroup for every eight tokens, k compares for every expert) 16384 took 23.6 us.
+//
 // Gradient of one chunk's tokens: LANES lanes hold a token's row from the read of its logits to the write of its
 // gradient; lane j < k holds slot j (k <= LANES).
 template <int PL, int LANES>
-__global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) {
-    constexpr int R = kThreads / LANES;
+__global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(BalanceArgs a) {
+    constexpr int R = kGradThreads / LANES;
+    __shared__ float s_row[R * LANES * PL];
     int64_t first, last;
     const int run = find_chunk<true>(a, &first, &last);
     const int tid = threadIdx.x, lane = tid % LANES, group = tid / LANES;
@@ -275,7 +362,7 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) 
     for (int u = 0; u < PL; ++u) f[u] = 0.0f;
     if (first < last && run >= 1 && run <= a.S) {
         const int s = run - 1;
-        const float inv = 1.0f / (float)(seq_start(a, s + 1) - seq_start(a, s));
+        const float inv = 1.0f / (float)(int)(seq_start(a, s + 1) - seq_start(a, s));
         if (a.d_balance != nullptr) {
             gb = a.d_balance[s] * inv;
             const float w = inv * ((float)a.E / (float)a.k);
@@ -287,21 +374,32 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) 
         }
         if (a.d_z != nullptr) gz = a.d_z[s] * inv;
     }
+    // the next token's reads are on their way while one is computed
+    float next[PL], g_next = 0.0f;
+    int e_next = -1;
+    auto fetch = [&](int64_t t) {
+        if (t >= last) return;
+        load_logits<PL, LANES>(a, t, lane, next);
+        if (a.d_w != nullptr && lane < a.k) {
+            e_next = a.idx[t * a.k + lane];
+            g_next = a.d_w[t * a.k + lane];
+        }
+    };
+    fetch(first + group);
     for (int64_t t = first + group; t < last; t += R) {
         TokenProbs<PL, LANES> tp;
-        load_logits<PL, LANES>(a, t, lane, tp.l);
-        int e_j = -1;
-        float l_j = kNegInf, g_j = 0.0f;
-        if (a.d_w != nullptr && lane < a.k) {
-            e_j = a.idx[t * a.k + lane];
-            g_j = a.d_w[t * a.k + lane];
-            if (e_j >= 0 && e_j < a.E) l_j = a.logits[t * a.E + e_j];
-            if (!(l_j > kNegInf)) {                    // no expert, or one that takes no part
-                e_j = -1;
-                l_j = kNegInf;
-                g_j = 0.0f;
-            }
+#pragma unroll
+        for (int u = 0; u < PL; ++u) tp.l[u] = next[u];
+        int e_j = e_next;
+        float l_j = kNegInf, g_j = g_next;
+        if (e_j >= 0 && e_j < a.E) l_j = a.logits[t * a.E + e_j];
+        fetch(t + R);
+        if (!(l_j > kNegInf)) {                        // no expert, or one that takes no part
+            e_j = -1;
+            l_j = kNegInf;
+            g_j = 0.0f;
         }
+        live_logits<PL, LANES>(a, lane, tp.l);
         token_probs(a, tp);
         float d[PL], fp = 0.0f;
 #pragma unroll
@@ -312,7 +410,6 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) 
         for (int u = 0; u < PL; ++u) {
             d[u] = gb * tp.p[u] * tp.slope[u] * (f[u] - fp);
             if (a.d_z != nullptr) d[u] += gl * tp.soft[u];
-            if (tp.l[u] == kNegInf) d[u] = 0.0f;
         }
         if (a.d_w != nullptr) {
             float score = 0.0f, slope = 1.0f;
@@ -324,7 +421,7 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) 
                     else score = exp_from(l_j, top);
                 }
                 const float sum = row_sum<LANES>(score);
-                score = sum > 0.0f ? score / sum : 0.0f;
+                score = sum > 0.0f ? score * rcp(sum) : 0.0f;
                 g_j -= row_sum<LANES>(g_j * score);
             } else if (l_j > kNegInf) {
                 if (a.sigmoid) sigmoid_of(l_j, &score, &slope);
@@ -336,13 +433,31 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) 
 #pragma unroll
                 for (int u = 0; u < PL; ++u) d[u] -= tp.soft[u] * all;
             }
-            for (int j = 0; j < a.k; ++j) {
-                const int e = __shfl(e_j, j, LANES);
-                const float v = __shfl(d_j, j, LANES);
+            // to the lanes that hold the experts, through the token's row in LDS, where every slot first leaves its
+            // lane: one that finds another there shares its expert, and then the slots are added one by one
+            float* const row = s_row + group * (PL * LANES);
+            int* const who = reinterpret_cast<int*>(row);
 #pragma unroll
-                for (int u = 0; u < PL; ++u)
-                    if (e == lane + LANES * u) d[u] += v;
+            for (int u = 0; u < PL; ++u) row[lane + LANES * u] = 0.0f;
+            wave_lds_sync();
+            if (e_j >= 0) who[e_j] = lane;
+            wave_lds_sync();
+            const bool shared = e_j >= 0 && who[e_j] != lane;
+            if (__any(shared)) {
+                for (int j = 0; j < a.k; ++j) {
+                    const int e = __shfl(e_j, j, LANES);
+                    const float v = __shfl(d_j, j, LANES);
+#pragma unroll
+                    for (int u = 0; u < PL; ++u)
+                        if (e == lane + LANES * u) d[u] += v;
+                }
+            } else {
+                if (e_j >= 0) row[e_j] = d_j;
+                wave_lds_sync();
+#pragma unroll
+                for (int u = 0; u < PL; ++u) d[u] += row[lane + LANES * u];
             }
+            wave_lds_sync();                          // read before the next token's zeros
         }
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
@@ -352,26 +467,55 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(BalanceArgs a) 
     }
 }
 
-// Experts a lane: a token takes 16 lanes up to 16 experts, 32 up to 32, a wave beyond.
+// Lanes of a token and experts of a lane: 16 lanes hold up to 256 experts, so that four tokens share a wave's exchanges
+// between lanes (the gradient, which keeps six numbers an expert: 8 a lane on up to 64 lanes); a few tokens, and the
+// slots of k > 16, take as many lanes as the experts fill.  Loss and gradient, us, narrow against wide, sigmoid:
+// 2048 x 256 12.7 + 6.3 against 12.1 + 6.0, 4096 x 256 12.9 + 7.3 against 12.6 + 7.1, 8192 x 256 13.9 + 9.2 against
+// 14.2 + 10.3, 16384 x 256 14.1 + 15.3 against 16.5 + 17.4, 16384 x 60 10.2 + 7.3 against 13.4 + 12.7.
+bool many_tokens(int64_t T, int k) { return T > 4096 && k <= 16; }
+
 template <typename F>
-void with_layout(int E, F go) {
-    if (E <= 16) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{});
-    else if (E <= 32) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 32>{});
-    else if (E <= 64) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 64>{});
-    else if (E <= 128) go(std::integral_constant<int, 2>{}, std::integral_constant<int, 64>{});
-    else if (E <= 256) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 64>{});
-    else if (E <= 512) go(std::integral_constant<int, 8>{}, std::integral_constant<int, 64>{});
-    else go(std::integral_constant<int, 16>{}, std::integral_constant<int, 64>{});
+void with_layout(int E, bool many, bool grad, F go) {
+    auto as = [&](auto pl, auto lanes) { go(pl, lanes); };
+    using std::integral_constant;
+    if (E <= 16) return as(integral_constant<int, 1>{}, integral_constant<int, 16>{});
+    if (E > 512) return as(integral_constant<int, 16>{}, integral_constant<int, 64>{});
+    if (many) {
+        if (E <= 32) as(integral_constant<int, 2>{}, integral_constant<int, 16>{});
+        else if (E <= 64) as(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+        else if (E <= 128) as(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+        else if (grad && E <= 256) as(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+        else if (grad) as(integral_constant<int, 8>{}, integral_constant<int, 64>{});
+        else if (E <= 256) as(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+        else as(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+    } else {
+        if (E <= 32) as(integral_constant<int, 1>{}, integral_constant<int, 32>{});
+        else if (E <= 64) as(integral_constant<int, 1>{}, integral_constant<int, 64>{});
+        else if (E <= 128) as(integral_constant<int, 2>{}, integral_constant<int, 64>{});
+        else if (E <= 256) as(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+        else as(integral_constant<int, 8>{}, integral_constant<int, 64>{});
+    }
 }
 
-// Tokens of a chunk: about 256 chunks, one a compute unit, of at most 4096 tokens, whose fp32 sums stay short.
-int loss_chunk(int64_t T) { return (int)std::min<int64_t>(std::max<int64_t>(8, (T + 255) / 256), 4096); }
+// Tokens that a workgroup of the gradient takes at a time in that layout.
+int tokens_at_once(int E, bool many) {
+    int n = 0;
+    with_layout(E, many, true, [&](auto, auto lanes) { n = kGradThreads / decltype(lanes)::value; });
+    return n;
+}
+
+// Tokens of a chunk: about 128 chunks, since one workgroup adds all of a sequence's (64, 128 and 256 of them, us: one
+// sequence of 4096 x 256 12.6, 11.6, 12.8, of 8192 x 256 13.4, 12.3, 13.9; four of 16384 tokens 18.3, 14.4, 14.3), of at
+// most 4096 tokens, whose fp32 sums stay short.
+constexpr int64_t kLossChunks = 128;
+int loss_chunk(int64_t T) { return (int)std::min<int64_t>(std::max<int64_t>(8, (T + kLossChunks - 1) / kLossChunks), 4096); }
 int64_t loss_chunks(int64_t T, int S) { return T / loss_chunk(T) + S; }
 
-// Gradient: no sums to leave, so chunks are what a workgroup takes at a time until the launch is large.
-int grad_chunk(int64_t T, int E) {
-    const int64_t at_once = E <= 16 ? 32 : E <= 32 ? 16 : 8;
-    return (int)((T + 65536 * at_once - 1) / (65536 * at_once) * at_once);
+// Gradient: no sums to leave, so chunks are what a workgroup takes at a time, or more where the launch has the waves to
+// fill the chip all the same.
+int grad_chunk(int64_t T, int E, int k) {
+    const int64_t at_once = tokens_at_once(E, many_tokens(T, k));
+    return (int)(at_once * std::max<int64_t>(1, T / (at_once * kGradWgs)));
 }
 
 struct LossWs {
@@ -380,10 +524,11 @@ struct LossWs {
 LossWs loss_ws(int64_t T, int E, int S) {
     auto align = [](size_t v) { return (v + 255) & ~(size_t)255; };
     // no fewer than loss_chunks(T, S), and growing with T
-    const size_t rows = (size_t)(std::max(std::min<int64_t>(T / 8, 256), T / 4096) + S);
+    const size_t rows = (size_t)(std::max(std::min<int64_t>(T / 8, kLossChunks), T / 4096) + S);
     LossWs w{};
-    w.n = align(rows * E * 4);
-    w.z = w.n + align(rows * E * 4);
+    const size_t E4 = (size_t)(E + 3) & ~(size_t)3;
+    w.n = align(rows * E4 * 4);
+    w.z = w.n + align(rows * E4 * 4);
     w.total = w.z + align(rows * 4);
     return w;
 }
@@ -449,13 +594,13 @@ extern "C" int dwdp_balance_loss(const float* logits, const int32_t* topk_idx, i
     a.z = z;
     hipStream_t st = as_stream(stream);
     if (T > 0) {
-        with_layout(E, [&](auto pl, auto lanes) {
+        with_layout(E, many_tokens(T, k), false, [&](auto pl, auto lanes) {
             hipLaunchKernelGGL((balance_chunk_kernel<decltype(pl)::value, decltype(lanes)::value>), dim3(a.n_chunks),
                                dim3(kThreads), 0, st, a);
         });
     }
-    int width = 64;
-    while (width < E) width *= 2;
+    int width = 16;
+    while (4 * width < E) width *= 2;
     hipLaunchKernelGGL(balance_finish_kernel, dim3(S), dim3(1024), 0, st, a, width);
     DWDP_LAUNCHED();
     return DWDP_OK;
@@ -490,7 +635,7 @@ extern "C" int dwdp_gate_backward(const float* logits, const int32_t* topk_idx, 
     a.S = S;
     a.sigmoid = gate->score == DWDP_SCORE_SIGMOID;
     a.offsets = seq_offsets;
-    a.chunk = grad_chunk(T, E);
+    a.chunk = grad_chunk(T, E, k);
     a.n_chunks = (int)(T / a.chunk + S + 2);
     a.counts = const_cast<int32_t*>(counts);
     a.d_w = d_w;
@@ -500,9 +645,9 @@ extern "C" int dwdp_gate_backward(const float* logits, const int32_t* topk_idx, 
     a.scale = gate->scale;
     a.d_logits = d_logits;
     hipStream_t st = as_stream(stream);
-    with_layout(E, [&](auto pl, auto lanes) {
+    with_layout(E, many_tokens(T, k), true, [&](auto pl, auto lanes) {
         hipLaunchKernelGGL((gate_backward_kernel<decltype(pl)::value, decltype(lanes)::value>), dim3(a.n_chunks),
-                           dim3(kThreads), 0, st, a);
+                           dim3(kGradThreads), 0, st, a);
     });
     DWDP_LAUNCHED();
     return DWDP_OK;

@@ -167,7 +167,7 @@ def test_balance_loss_workspace_grows(lib):
         sizes = [f(t, E, S) for t in ts]
         assert sizes == sorted(sizes) and f(ts[-1], E, S + 1) >= sizes[-1]
         # chunks of 8 .. 4096 tokens, one more for every sequence: 8 bytes an expert
-        assert all(n >= (min(t // max(8, -(-t // 256)), 256) + S) * E * 8 for t, n in zip(ts, sizes))
+        assert all(n >= (t // min(max(8, -(-t // 128)), 4096) + S) * E * 8 for t, n in zip(ts, sizes))
 
 
 def backward(lib, l=FAKE, i=FAKE2, T=4, E=8, g=None, dw=FAKE3, off=None, S=1, c=None, db=None, dz=None,
