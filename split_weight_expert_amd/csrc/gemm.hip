@@ -571,10 +571,11 @@ struct TileCtx {
 // while the other's MFMAs do.
 // 256-row fp8 tiles (compile-time option DWDP_FP8_BM256) take 64-byte K steps: a 128-byte step of 256
 // rows leaves room for only two ring slots
-constexpr int rowb_of(int BM, bool FP8) { return FP8 ? (BM >= 256 ? 64 : 128) : (BM == 32 ? 128 : 64); }
+constexpr int rowb_of(int BM, int prec) { return prec == kFp8 ? (BM >= 256 ? 64 : 128) : (BM == 32 ? 128 : 64); }
 
-template <int BM, int ROWB, bool FP8>
+template <int BM, int ROWB, int PREC>
 struct FragCfg {
+    static constexpr bool FP8 = PREC == kFp8;
     static constexpr int NW = (FP8 ? BM >= 128 : BM >= 256) ? 8 : 4;   // waves
     static constexpr int RH = NW / 4;                         // row parts (waves per column group)
     static constexpr int MI = BM / 32, MIW = MI / RH, NJ = 2; // m-blocks per tile / per wave
@@ -597,7 +598,15 @@ struct FragCfg {
     // once per tile
     static constexpr int BSC = FP8 ? NW * NJ * 64 : 0;        // floats
     static constexpr int EXTRA = BSC * 4;
-    static constexpr int FIT = (163840 - EXTRA) / STAGE;
+    // int8: a step's MFMAs take half as long for the same bytes, so what a tile spends outside its K loop (dispatch,
+    // lookup, the ring's fill, the epilogue) counts twice as much.  Its tiles of 64 and 128 rows take half of the LDS, so
+    // that one workgroup's K loop runs beside the other's ends.  Both GEMMs, us, two a compute unit of up to 128 rows
+    // against one of up to 256: 60 groups of 77 rows (H 2048, I 768) 86 against 101, of 200 rows 118 against 135;
+    // H 7168, I 2048: 65 groups of 138 rows 714 against 791, 257 of 286 4213 against 4572, 129 of 571 3617 against 3628;
+    // 8 of 2048 (H 2048, I 1024) 168 against 191, 17 of 4336 (H 7168, I 2048) 3431 against 3308, the one loss.
+    static constexpr int WG_PER_CU = PREC == kInt8 && BM >= 64 ? 2 : 1;
+    static constexpr int LDS = 163840 / WG_PER_CU;
+    static constexpr int FIT = (LDS - EXTRA) / STAGE;
     static constexpr int NS = FIT < 8 ? FIT : 8;              // ring slots
     // bf16 reuses a slot one step after its last read (P = NS - 2), so the DMA can be issued before
     // the step's closing LDS wait; fp8 reuses it right after the barrier (P = NS - 1)
@@ -711,7 +720,7 @@ template <int BM, int ROWB, int MA, int MWV, int KIND, int PREC, int WPOL>
 __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c, uint8_t* smem,
                                           const float* s_bscale) {
     constexpr bool FP8 = PREC == kFp8, INT8 = PREC == kInt8;
-    using C = FragCfg<BM, ROWB, FP8>;
+    using C = FragCfg<BM, ROWB, PREC>;
     using Acc = std::conditional_t<INT8, i32x16, f32x16>;
     using Operand = std::conditional_t<INT8, i32x4, bf16x8>;   // of one MFMA (bf16, int8)
     constexpr int NS = C::NS, P = C::P, NJ = C::NJ, CH = C::CH, BF = C::BF, STAGE = C::STAGE;
@@ -1261,11 +1270,11 @@ __device__ __forceinline__ void frag_tile(const GemmParams& p, const TileCtx& c,
 }
 
 template <int BM, int KIND, int PREC>
-__global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, PREC == kFp8), PREC == kFp8>::NW * 64), 1)
+__global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, PREC), PREC>::NW * 64), (FragCfg<BM, rowb_of(BM, PREC), PREC>::WG_PER_CU))
     void gemm_frag_kernel(GemmParams p) {
     constexpr bool FP8 = PREC == kFp8;
-    constexpr int ROWB = rowb_of(BM, FP8);
-    using C = FragCfg<BM, ROWB, FP8>;
+    constexpr int ROWB = rowb_of(BM, PREC);
+    using C = FragCfg<BM, ROWB, PREC>;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[C::NS * C::STAGE + C::EXTRA];
     float* s_bscale = reinterpret_cast<float*>(smem + C::NS * C::STAGE);   // fp8 only
 
@@ -1287,7 +1296,9 @@ __global__ __launch_bounds__((FragCfg<BM, rowb_of(BM, PREC == kFp8), PREC == kFp
         lin = *s_ticket;
         __syncthreads();
     } else {
-        lin = dealt_lin(KIND == kGemm1 ? DWDP_CLUSTER_GEMM1_LOG2 : DWDP_CLUSTER_GEMM2_LOG2);
+        // int8: 64 tiles run on an XCD at once, so GEMM2 takes GEMM1's clusters too (GEMM2 of 129 groups of 571 rows
+        // 1221 against 1247 us)
+        lin = dealt_lin(KIND == kGemm1 || PREC == kInt8 ? DWDP_CLUSTER_GEMM1_LOG2 : DWDP_CLUSTER_GEMM2_LOG2);
     }
     if (!decode_tile<BM, KIND>(p, c.t, lin)) return;
 #if DWDP_TILE_TRACE
@@ -1509,6 +1520,7 @@ int choose_bm(int dtype, int64_t rows, int groups) {
     if (dtype == DWDP_F32) return kBmF32;
     const int64_t mean = rows / groups;
     const int bm = mean >= 192 ? 256 : mean >= 96 ? 128 : mean >= 40 ? 64 : 32;
+    if (dtype == DWDP_INT8) return std::min(bm, 128);          // two of them share a compute unit (FragCfg)
 #ifdef DWDP_FP8_BM256
     return bm;
 #else
@@ -1552,8 +1564,7 @@ void launch_f32(const GemmParams& p, int64_t tiles, hipStream_t st) {
 
 template <int BM, int KIND, int PREC>
 void launch_dma(const GemmParams& p, int64_t tiles, hipStream_t st) {
-    constexpr bool FP8 = PREC == kFp8;
-    constexpr int threads = FragCfg<BM, rowb_of(BM, FP8), FP8>::NW * 64;
+    constexpr int threads = FragCfg<BM, rowb_of(BM, PREC), PREC>::NW * 64;
     hipLaunchKernelGGL((gemm_frag_kernel<BM, KIND, PREC>), dim3((unsigned)xcd_grid(tiles)), dim3(threads), 0, st, p);
 }
 
@@ -1586,7 +1597,7 @@ int launch_ffn(bool g1, bool g2, int prec, bool g2_wide, const int32_t* offsets,
             return DWDP_OK;
         }
     }
-    if (prec == kInt8) {
+    if constexpr (BM <= 128) if (prec == kInt8) {
         if (g1) {
             launch_dma<BM, kGemm1, kInt8>(p1, maxm * p1.NT, st);
             const int rc = quantize_rows_int8(p1.out, DWDP_F32, p2.a_nrows, p1.N, const_cast<uint8_t*>(p2.a),
@@ -1671,7 +1682,11 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
     hipStream_t st = as_stream(stream);
     uint8_t* base = static_cast<uint8_t*>(ws);
     const int bm = choose_bm(w_dtype, rows, n_groups);
-    const int64_t maxm = (rows + bm - 1) / bm + n_groups;
+    // at most this many m-tiles: a whole one for every bm rows, and a part of one for every group that has rows (workgroups
+    // beyond the tiles exit, but each takes a compute unit's LDS first: int8, one token of 65 groups, GEMM2 42 us of
+    // which 15 were theirs when the bound counted groups without rows)
+    auto most_tiles = [&](int64_t h) { return std::min(rows, rows / h + std::min<int64_t>(rows, n_groups)); };
+    const int64_t maxm = most_tiles(bm);
 
     GemmParams p1{};
     p1.a = static_cast<const uint8_t*>(x);
@@ -1696,7 +1711,7 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
     p1.out_scale = reinterpret_cast<float*>(base + L.a_scale);
 
     GemmParams p2 = p1;
-    p2.mtiles = w_dtype == DWDP_BF16 ? mt_group : mt_size;
+    p2.mtiles = w_dtype == DWDP_BF16 || w_dtype == DWDP_INT8 ? mt_group : mt_size;
     p2.a = base + L.a;
     p2.a_scale = reinterpret_cast<const float*>(base + L.a_scale);
     p2.a_rows = nullptr;
@@ -1709,6 +1724,7 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
     // fp8 GEMM2 takes super-blocks of 8 m-tiles (16K fp8 GEMM2 3.41-3.42 ms against 3.44-3.46 with 4;
     // bf16 GEMM2 was not faster with 1, 2 or 8)
     if (w_dtype == DWDP_FP8_E4M3) p2.msuper = DWDP_MSUPER_FP8_GEMM2;
+    if (w_dtype == DWDP_INT8) p2.msuper = 8;
     // 32-row tiles (a few rows per group, as in decode) share next to nothing: they draw tickets, so
     // that every XCD keeps taking tiles until none are left.  The schedule kernel zeroes both counters
     // (p2.ticket = p1.ticket + 1), and each launch's last draw resets its own.
@@ -1732,7 +1748,7 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
         // weight re-reads of 128-row tiles; GEMM1 stays at 128 rows (its per-block rescale made 256-row
         // tiles slower there)
         const bool g2_wide = DWDP_FP8_GEMM2_BM256 && fp8 && bm == 128 && rows / n_groups >= 192;
-        const int64_t maxm_wide = (rows + 255) / 256 + n_groups;
+        const int64_t maxm_wide = most_tiles(256);
         int rc;
         if (bm == 256)
             rc = launch_ffn<256>(g1, g2, prec, false, offsets, n_groups, p1, p2, mt_group, mt_size, maxm, maxm, st);
