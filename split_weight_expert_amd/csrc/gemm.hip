@@ -1520,7 +1520,11 @@ int choose_bm(int dtype, int64_t rows, int groups) {
     if (dtype == DWDP_F32) return kBmF32;
     const int64_t mean = rows / groups;
     const int bm = mean >= 192 ? 256 : mean >= 96 ? 128 : mean >= 40 ? 64 : 32;
-    if (dtype == DWDP_INT8) return std::min(bm, 128);          // two of them share a compute unit (FragCfg)
+    // int8: two tiles of 64 or 128 rows share a compute unit (FragCfg), so 64 rows pay from 16 on, us against 32 rows: 60
+    // groups of 30 rows (H 2048, I 768) 71 and 77, 33 of 22 (H 7168, I 2048) 264 and 271.  128 rows from 96 on; below,
+    // it goes by how the tiles fill the chip, 128 rows against 64: 33 groups of 90 rows (H 7168, I 2048) 317 and 378, of
+    // 75 (H 4096, I 1024) 118 and 105, 8 of 87 (H 1024, I 512) 33 and 24.
+    if (dtype == DWDP_INT8) return mean >= 96 ? 128 : mean >= 16 ? 64 : 32;
 #ifdef DWDP_FP8_BM256
     return bm;
 #else
