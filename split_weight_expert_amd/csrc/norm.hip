@@ -250,6 +250,10 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
 // codes: 16384 rows are 1061 MB in 184 us, 5.8 TB/s; combine of 8192 rows, k = 8 and a shared row, 1470 MB in 271 us,
 // 5.4 TB/s (a plain copy reaches 4.9); fp32 rows, sum and y: 4096 tokens 1409 MB in 298 us, 4.7 TB/s.  A few rows are
 // bound by latency: one row 3.8 us, of which an empty kernel takes 2.3.  Reading the rows twice (norm_two_pass_kernel) took 241 us and 495 us.
+// With a branch the row is reduced twice (three times with int8 codes) and its columns read two or three more arrays,
+// which stay in L2: still one read and one write of each row.  7168-wide bf16, sum and y: 16384 rows of a dense branch 940 MB in
+// 180 us, 5.2 TB/s (with int8 codes 1057 MB in 209); combine of 8192, k = 8 and a shared row, with codes, 1470 MB in 279 us,
+// 5.3 TB/s; one row 6.8 us, 64 rows 7.4.  Reading the columns ahead of the reductions did not help (7.0 and 7.5).
 template <bool COMBINE, bool BRANCH, bool BF16, bool EVEN, int C, int LANES>
 __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
     static_assert(!COMBINE || EVEN, "combine takes rows of a multiple of 8");
