@@ -207,7 +207,7 @@ size_t dwdp_balance_loss_workspace_bytes(int64_t T, int E, int S);
  *             not renormalised: scale d_w_j score_j h_j to the logit of slot j's expert; for softmax also
  *                 - softmax(l)_i sum_j scale d_w_j score_j to every logit
  * An expert that several slots of a token name takes the sum of theirs.  Slots outside [0, E) and logits of
- * NaN or -inf take no part and get 0; a logit of +inf makes the z loss's gradient of its token NaN.
+ * NaN or -inf take no part and get 0; a logit of +inf makes the z loss's gradient of its token (d_z not 0) NaN.
  *   d_w [T,k], d_balance [S], d_z [S] fp32, each NULL if there is none of it (not all three).
  *   counts [S,E]: dwdp_balance_loss's (needed with d_balance).  seq_offsets, S: as there; tokens of no
  *   sequence get the gradient of their weights alone.  d_logits [T,E] fp32 (written, not added to).

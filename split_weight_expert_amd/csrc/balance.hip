@@ -100,7 +100,7 @@ struct TokenProbs {
     float soft[PL];       // softmax(l)
     float p[PL];          // soft, or normalised sigmoids
     float slope[PL];      // 1, or 1 - sigmoid(l)
-    float top, inv;       // largest logit; 1 / sum of e^(l - top)
+    float top, inv;       // largest logit; softmax: 1 / sum of e^(l - top)
     float lse;            // logsumexp(l), 0 for a token without a live logit
 };
 
@@ -166,14 +166,12 @@ __device__ __forceinline__ void token_probs(const BalanceArgs& a, TokenProbs<PL,
         }
         sum = row_sum<LANES>(sum);
         t.lse = __logf(sum);
-        t.inv = rcp(sum);
-        const float f = rcp(row_sum<LANES>(total));
+        const float inv = rcp(sum), f = rcp(row_sum<LANES>(total));
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
-            t.soft[u] *= t.inv;
+            t.soft[u] *= inv;
             t.p[u] *= f;
         }
-        t.inv *= __expf(top);
         return;
     }
     if (top < __builtin_huge_valf()) {
@@ -405,7 +403,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(BalanceArgs
 #pragma unroll
         for (int u = 0; u < PL; ++u) fp += f[u] * tp.p[u];
         fp = row_sum<LANES>(fp);
-        const float gl = gz * 2.0f * tp.lse;
+        const float gl = gz == 0.0f ? 0.0f : gz * 2.0f * tp.lse;      // lse may be infinite where there is no loss
 #pragma unroll
         for (int u = 0; u < PL; ++u) {
             d[u] = gb * tp.p[u] * tp.slope[u] * (f[u] - fp);

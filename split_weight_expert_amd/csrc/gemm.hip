@@ -613,6 +613,7 @@ struct FragCfg {
     static constexpr int P = FP8 ? NS - 1 : NS - 2;           // steps in flight ahead of the MFMAs
     static_assert(BM % 32 == 0 && (ROWB == 64 || ROWB == 128), "tile shape");
     static_assert(P >= 1, "ring too shallow");
+    static_assert(NS * STAGE >= BM * 512, "the epilogue stages 512 bytes a row in the ring");
     static_assert(BI % RH == 0 && MI % RH == 0, "waves split the tile evenly");
 };
 

@@ -263,6 +263,61 @@ def test_no_tokens(api):
     api.gate_backward(l, idx, api.Gate(k=2), torch.empty(0, 10, device=DEV), torch.empty(0, 2, device=DEV))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_padding_of_any_content(api, score):
+    """Rows before the first and behind the last sequence may hold anything: they change no loss, and get no gradient of one."""
+    T, E, k = 90, 24, 3
+    l, idx, g = routed(T, E, k, 31)
+    off = [4, 30, 70]
+    gate = api.Gate(k=k, score=score)
+    a, offd, S = run_loss(api, l.to(DEV), idx.to(DEV), gate, off)
+    db, dz = torch.randn(2, generator=g).to(DEV), torch.randn(2, generator=g).to(DEV)
+    want = torch.empty(T, E, device=DEV)
+    api.gate_backward(l.to(DEV), idx.to(DEV), gate, want, None, a["counts"][:S], db, dz, offd)
+    for n, v in enumerate((float("inf"), float("nan"), float("-inf"), torch.finfo(torch.float32).max)):
+        l[n], l[70 + n], l[80, n] = v, v, v
+        idx[n], idx[70 + n] = -(1 << 31) + n, (1 << 31) - 1 - n
+    b, _, _ = run_loss(api, l.to(DEV), idx.to(DEV), gate, off)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    out = torch.empty(T, E, device=DEV)
+    api.gate_backward(l.to(DEV), idx.to(DEV), gate, out, None, b["counts"][:S], db, dz, offd)
+    assert torch.equal(out, want) and (out[:4] == 0).all() and (out[70:] == 0).all()
+
+
+def test_two_calls_at_once(api):
+    """Calls on two streams, each with a workspace of its own, enqueued without waiting for one another."""
+    gate = api.Gate(k=4, score="sigmoid")
+    sets = []
+    for i in range(2):
+        l, idx, _ = routed(6000 + i, 200, 4, i)
+        sets.append((l.to(DEV), idx.to(DEV)))
+    want = [run_loss(api, *s, gate)[0] for s in sets]
+    ws = [torch.empty(api.balance_loss_workspace_bytes(6001, 200, 1), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(run_loss(api, *sets[i], gate, ws=ws[i])[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o[n], want[i][n]) for i in range(2) for o in got[i] for n in o)
+
+
+def test_a_long_batch(api):
+    """Chunks of 4096 tokens: 2^20 + 3 tokens in two sequences, against sums in fp64."""
+    T, E, k = (1 << 20) + 3, 8, 2
+    g = torch.Generator(device=DEV).manual_seed(3)
+    l = torch.randn(T, E, device=DEV, generator=g)
+    idx = l.topk(k, 1).indices.int()
+    o, _, S = run_loss(api, l, idx, api.Gate(k=k), [0, 5, T])
+    p = torch.softmax(l.double(), 1)
+    for s, (a, b) in enumerate(((0, 5), (5, T))):
+        assert torch.equal(o["counts"][s].long(), torch.bincount(idx[a:b].reshape(-1).long(), minlength=E))
+        # D is below 12: (2.2 * 12 + 12) 2^-23 and the sums' 552 2^-24
+        assert torch.allclose(o["probs"][s].double(), p[a:b].mean(0), rtol=(2.2 * 12 + 12) * 2 * U + 552 * U, atol=0)
+
+
 def test_offsets_out_of_range_stay_in_bounds(api):
     """Offsets below 0 or past T are taken as 0 and T."""
     l, idx, g = routed(100, 16, 2, 1)
