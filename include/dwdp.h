@@ -38,7 +38,8 @@
  *     DWDP_ERR_INVALID_ARG ("too large"), a call whose tile grid would not fit:
  *     the router above ceil(T/64) * ceil(E/64) ~ 2^24 tiles (about 2^26 tokens at
  *     E = 1024), the grouped FFN above (rows/BM + n_groups) * max(2I, H)/256 ~ 2^23
- *     tiles (BM the tile height, 256 at prefill: about 75M rows at H = 7168).
+ *     tiles (BM the tile height, 256 at prefill: about 75M rows at H = 7168; int8
+ *     64 or 128).
  *
  * Layouts (row-major, C order)
  *   x          [T, H]            tokens, bf16 (f32 for the f32 path)

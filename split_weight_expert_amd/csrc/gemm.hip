@@ -1517,15 +1517,19 @@ constexpr int kBnDma = 256;
 constexpr int kBmF32 = 64, kBnF32 = 64;
 constexpr int kBmRouter = 64, kBnRouter = 64;
 
-int choose_bm(int dtype, int64_t rows, int groups) {
+int choose_bm(int dtype, int64_t rows, int groups, int I) {
     if (dtype == DWDP_F32) return kBmF32;
     const int64_t mean = rows / groups;
     const int bm = mean >= 192 ? 256 : mean >= 96 ? 128 : mean >= 40 ? 64 : 32;
-    // int8: two tiles of 64 or 128 rows share a compute unit (FragCfg), so 64 rows pay from 16 on, us against 32 rows: 60
-    // groups of 30 rows (H 2048, I 768) 71 and 77, 33 of 22 (H 7168, I 2048) 264 and 271.  128 rows from 96 on; below,
-    // it goes by how the tiles fill the chip, 128 rows against 64: 33 groups of 90 rows (H 7168, I 2048) 317 and 378, of
-    // 75 (H 4096, I 1024) 118 and 105, 8 of 87 (H 1024, I 512) 33 and 24.
-    if (dtype == DWDP_INT8) return mean >= 96 ? 128 : mean >= 16 ? 64 : 32;
+    if (dtype == DWDP_INT8) {
+        // Two tiles of 64 or 128 rows share a compute unit (FragCfg).  128 rows where GEMM1's tiles fill these 512 places,
+        // or with several tiles a group half of them.  Both GEMMs, us, 128 rows against 64: 33 groups of 90 (H 7168, I 2048,
+        // 528 tiles) 317 and 378, 60 of 77 (2048, 768, 360 tiles) 88 and 85, 16 of 125 (4096, 1024, 128 tiles) 82 and
+        // 69, 8 of 250 (7168, 2048, 256 tiles) 166 and 196, 8 of 250 (1024, 512, 64 tiles) 33 and 25.  64 rows against 32:
+        // 60 groups of 30 (2048, 768) 71 and 77, 33 of 22 (7168, 2048) 264 and 271.
+        const int64_t tiles = groups * ((mean + 127) / 128) * (I / 128);
+        return mean >= 64 && tiles >= (mean > 128 ? 256 : 512) ? 128 : mean >= 16 ? 64 : 32;
+    }
 #ifdef DWDP_FP8_BM256
     return bm;
 #else
@@ -1686,7 +1690,7 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
         return fail(DWDP_ERR_WORKSPACE, "dwdp_moe_grouped_ffn: workspace too small (need " + std::to_string(L.total) + ")");
     hipStream_t st = as_stream(stream);
     uint8_t* base = static_cast<uint8_t*>(ws);
-    const int bm = choose_bm(w_dtype, rows, n_groups);
+    const int bm = choose_bm(w_dtype, rows, n_groups, I);
     // at most this many m-tiles: a whole one for every bm rows, and a part of one for every group that has rows (workgroups
     // beyond the tiles exit, but each takes a compute unit's LDS first: int8, one token of 65 groups, GEMM2 42 us of
     // which 15 were theirs when the bound counted groups without rows)

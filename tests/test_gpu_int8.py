@@ -148,10 +148,12 @@ class Layer:
         return flips
 
 
-# rows per group: empty groups, single rows, tails of every 32-row block, and every tile height (mean rows from 40, 96, 192)
+# rows per group: empty groups, single rows, tails of every 32-row block, and every tile height
 ROWS = [([1], 256, 128), ([0, 3, 0, 1, 33, 0], 256, 128), ([31, 32, 33, 64, 65, 1, 0, 20], 512, 256),
         ([50, 90, 1, 63, 64, 129], 768, 128), ([100, 200, 0, 161, 97, 128], 256, 384), ([300, 0, 257, 511, 33, 224, 700], 512, 256),
-        ([5, 3, 2, 0, 8, 1, 1, 9], 7168, 2048), ([260, 190, 250], 2304, 640), ([2000], 256, 128), ([64, 40, 0, 100], 256, 1152)]
+        ([5, 3, 2, 0, 8, 1, 1, 9], 7168, 2048), ([260, 190, 250], 2304, 640), ([2000], 256, 128), ([64, 40, 0, 100], 256, 1152),
+        # tiles of 128 rows: 512 of them with groups of 64 or more, 256 with groups of more than 128
+        ([64, 65, 127, 128, 0, 63, 100, 70] * 4, 256, 2048), ([129, 255, 300, 31, 161, 96, 0, 330] * 2, 512, 1024)]
 
 
 @pytest.mark.parametrize("rows,H,I", ROWS)
