@@ -1509,8 +1509,8 @@ __global__ __launch_bounds__(256) void gemm_f32_kernel(GemmParams p) {
 }
 
 // ------------------------------------------------------------------------------ configs
-// Expert GEMMs (bf16, fp8): gemm_frag_kernel, BM x 256 tiles with BM = 32, 64, 128 or 256 (fp8: at
-// most 128) picked from the mean rows per group (decode batches give groups of a few rows).
+// Expert GEMMs (bf16, fp8, int8): gemm_frag_kernel, BM x 256 tiles with BM = 32, 64, 128 or 256 (fp8 and
+// int8: at most 128) picked from the mean rows per group (decode batches give groups of a few rows).
 // f32: 64 x 64 FMA tiles.
 // Router (bf16): router_dma_kernel or router_mfma_kernel, 64 x 64 tiles.
 constexpr int kBnDma = 256;
@@ -1706,7 +1706,7 @@ int grouped_ffn(int stage, const dwdp_expert_ptrs* table, int n_groups, const in
     p1.offsets = offsets;
     p1.mprefix = reinterpret_cast<int32_t*>(base + L.pre);
     // GEMM1 walks the groups by size (bf16: measured ~1.5% faster at 8K tokens).  GEMM2 keeps group
-    // order for bf16 (slower by size) and walks by size otherwise.  The order moves no result bit.
+    // order for bf16 (slower by size) and int8, and walks by size otherwise.  The order moves no result bit.
     MTile* mt_group = reinterpret_cast<MTile*>(base + L.mt);
     MTile* mt_size = reinterpret_cast<MTile*>(base + L.mt_by_size);
     p1.mtiles = mt_size;
