@@ -57,7 +57,7 @@ __global__ __launch_bounds__(1024) void quant_row_kernel(QuantArgs a) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = (c * bx + tx) * 8;
-            if (col < a.cols) *reinterpret_cast<uint2*>(a.q + t * a.cols + col) = int8x8(v[c], s);
+            if (col < a.cols) *reinterpret_cast<uint2*>(a.q + t * a.cols + col) = int8x8<true>(v[c], s);
         }
         if (tx == 0) a.scale[t] = s.scale;
     }
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(1024) void quant_wide_kernel(QuantArgs a) {
         const Int8Scale s = int8_scale(m);
         for (uint32_t c = tx * 8; c < (uint32_t)a.cols; c += 1024 * 8) {
             unpack<BF16>(load_raw<BF16, true>(x, c), v);
-            *reinterpret_cast<uint2*>(a.q + t * a.cols + c) = int8x8(v, s);
+            *reinterpret_cast<uint2*>(a.q + t * a.cols + c) = int8x8<true>(v, s);
         }
         if (tx == 0) a.scale[t] = s.scale;
     }

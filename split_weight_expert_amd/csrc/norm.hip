@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
                 for (uint32_t c = tid * 8; c < (uint32_t)a.H; c += 256 * 8) {
                     load(c, z);
                     norm8<BF16, EVEN>(a, t, c, z, r);
-                    *reinterpret_cast<uint2*>(a.q + t * a.H + c) = int8x8(z, s);
+                    *reinterpret_cast<uint2*>(a.q + t * a.H + c) = int8x8<false>(z, s);
                 }
                 if (tid == 0) a.q_scale[t] = s.scale;
                 continue;
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     const int col = (c * bx + tx) * 8;
-                    if (col < a.H) *reinterpret_cast<uint2*>(a.q + t * a.H + col) = int8x8(z[c], s);
+                    if (col < a.H) *reinterpret_cast<uint2*>(a.q + t * a.H + col) = int8x8<false>(z[c], s);
                 }
                 if (tx == 0) a.q_scale[t] = s.scale;
                 continue;

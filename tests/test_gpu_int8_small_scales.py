@@ -71,3 +71,20 @@ def test_half_of_the_largest(dt):
     np.testing.assert_array_equal(s.cpu().numpy(), ws)
     np.testing.assert_array_equal(q.cpu().numpy(), want)
     assert set(np.unique(want[:, 1])) == {63, 64}
+
+
+@pytest.mark.parametrize("T,H", [(300, 136), (40, 1000), (9, 7168), (3, 40000)])
+@pytest.mark.parametrize("exponent", [-126, -121, -112])
+def test_norms_divide_as_ieee_does(T, H, exponent):
+    """The norm's codes are those of its fp32 output, whose scale a small weight brings down."""
+    from split_weight_expert_amd import api
+    g = torch.Generator().manual_seed(H)
+    # whole numbers over few values: many quotients at and beside ties
+    x = torch.randint(-254, 255, (T, H), generator=g).float()
+    x[:, 0] = 254
+    w = torch.full((H,), 2.0 ** exponent)
+    y, q, s = torch.empty(T, H, device=DEV), torch.empty(T, H, dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    api.branch_add_rmsnorm(x.to(DEV), None, None, w.to(DEV), 1e-6, y=y, q=q, q_scale=s)
+    want, ws = o8.rows(y.cpu().numpy())
+    np.testing.assert_array_equal(s.cpu().numpy(), ws)
+    np.testing.assert_array_equal(q.cpu().numpy(), want)
