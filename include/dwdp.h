@@ -195,9 +195,10 @@ int dwdp_quantize_tokens_fp8(const void* x, int64_t T, int H, void* q, float* q_
  *   device only; no host synchronisation happens.
  *   ws: dwdp_workspace_bytes(DWDP_OP_GROUPED_FFN, ...) bytes.  After GEMM1 it
  *     begins with A [rows, I] row-major in the activation type (fp32, bf16, or
- *     E4M3 or int8 codes), followed for FP8 at the next 256-byte boundary by A's scales
- *     [rows, I/128] fp32, for INT8 by A's scales [rows] fp32; the tile schedule sits
- *     after them. */
+ *     E4M3 or int8 codes).  Then, each from the next 256-byte boundary on: for FP8
+ *     A's scales [rows, I/128] fp32; for INT8 A's scales [rows] fp32 and the fp32 A
+ *     [rows, I] that the codes are made of; the tile schedule.  INT8's fp32 A is four
+ *     times its codes, so its workspace is 2.5 times BF16's. */
 int dwdp_moe_grouped_ffn(const dwdp_expert_ptrs* table, int n_groups, const int32_t* offsets,
                          const void* x_perm, const float* x_perm_scale, int64_t rows, int H, int I,
                          int w_dtype, void* y_perm, void* ws, size_t ws_bytes, void* stream);
@@ -230,7 +231,8 @@ int dwdp_moe_grouped_ffn_tokens(int stage, const dwdp_expert_ptrs* table, int n_
  * dwdp_moe_grouped_ffn_tokens computes with the same arguments (bitwise), and rejects with
  * DWDP_ERR_WORKSPACE, before anything is enqueued, a shape whose workspace
  * (dwdp_workspace_bytes(DWDP_OP_GROUPED_FFN, ...)) exceeds that size -- with bf16 weights and I = 2048
- * about 16K permuted rows, e.g. a decode batch of up to ~1800 tokens at top-8 plus a shared expert.
+ * about 16K permuted rows, e.g. a decode batch of up to ~1800 tokens at top-8 plus a shared expert (int8:
+ * about 6.5K rows, ~720 tokens).
  * Every call on one GPU shares that GPU's array, which keeps the last call's contents: a stage-2 call
  * reads the A left by the last stage-1 call on that GPU, and calls whose executions overlap on one GPU
  * (other streams, other threads) race on the array and give undefined results. */
