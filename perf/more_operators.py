@@ -169,8 +169,6 @@ def prepare(case, seed):
     s = {"case": c}
     make = {"boundary": _prepare_rows, "branch": _prepare_rows, "balance": _prepare_balance, "experts": _prepare_experts}
     make[c["op"]](s, c, g, randn)
-    if own:
-        s["own"] = _buffers(s)
     return s
 
 
@@ -328,7 +326,9 @@ def _buffers(s):
 
 
 def _own(s):
-    b = s["own"]
+    b = s.get("own")
+    if b is None:
+        b = s["own"] = _buffers(s)
     c, api = s["case"], b["api"]
     op = c["op"]
     if op == "balance":
