@@ -237,8 +237,9 @@ __device__ __forceinline__ void load_logits(const BalanceArgs& a, int64_t tok, i
 }
 
 // Bound by latency up to some thousand tokens (an empty kernel takes 2.3 us, two of them and their parts' dependent reads
-// 7 us), and by instructions, not bytes, beyond: sigmoids, 256 experts, 65536 tokens are 67 MB in 28 us.  16384 tokens in
-// four sequences 14.4 us, of which the second launch takes 6.  Before (a wave a token, exact divisions, reads parted by
+// 7 us), and by vector instructions on the compute units that have a chunk beyond: sigmoids, 256 experts, 65536 tokens are
+// 67 MB in 30 us, 132 workgroups whose units' SIMDs are 82% busy, while the others have none (kLossChunks).  16384 tokens
+// in four sequences 14.3 us, of which the second launch takes 5.  Before (a wave a token, exact divisions, reads parted by
 // branches) 25.9 us.
 //
 // Sums of one chunk: lanes add their experts' probabilities over the tokens, then the token groups meet in LDS.
@@ -360,7 +361,8 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceArgs a, int
     }
 }
 
-// Bound as the loss is: 64 tokens of 256 experts 4.7 us, 16384 15.3 us (50 MB at 3.3 TB/s), 65536 36 us (3.7 TB/s).
+// Bound by latency, then by vector instructions (SIMDs 89% busy on the whole chip at 65536 tokens): 64 tokens of 256 experts
+// 4.8 us, 16384 15.3 us (34.6 MB read and written, 2.3 TB/s), 65536 36 us (138 MB, 3.8 TB/s).
 // Before (a workgroup for every eight tokens, k compares for every expert) 16384 took 23.6 us.
 //
 // Gradient of one chunk's tokens: LANES lanes hold a token's row from the read of its logits to the write of its

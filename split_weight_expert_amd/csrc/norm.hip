@@ -163,7 +163,9 @@ __device__ __forceinline__ void load_z(const NormArgs& a, int64_t t, int col, co
 // twice (for the sum of squares, then to write), each element by the same thread, so that outputs may take their
 // inputs' place.  Columns are counted without a sign: the step past the last one of a row of nearly 2^31 elements is
 // still a number that lies behind the row.  A thread adds H / 2048 vectors: in fp32 the sum of like terms
-// was off by 3e-4 at 2^25 elements and by 9% at 2^31.  A branch's norm takes one more pass, and so do int8 codes.
+// was off by 3e-4 at 2^25 elements and by 9% at 2^31.  A branch's norm takes one more pass, and so do int8 codes: combine of
+// 1024 rows of 20480 bf16, k = 8 and a shared row, 201 us without a branch, 279 with its norm, 368 with codes too; 1024
+// dense rows of 40960 85, 102 and 135.
 template <bool COMBINE, bool BRANCH, bool BF16, bool EVEN>
 __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
     __shared__ int32_t s_row[kMaxK];
@@ -253,7 +255,9 @@ __global__ __launch_bounds__(256) void norm_two_pass_kernel(NormArgs a) {
 // With a branch the row is reduced twice (three times with int8 codes) and its columns read two or three more arrays,
 // which stay in L2: still one read and one write of each row.  7168-wide bf16, sum and y: 16384 rows of a dense branch 940 MB in
 // 180 us, 5.2 TB/s (with int8 codes 1057 MB in 209); combine of 8192, k = 8 and a shared row, with codes, 1470 MB in 279 us,
-// 5.3 TB/s; one row 6.8 us, 64 rows 7.4.  Reading the columns ahead of the reductions did not help (7.0 and 7.5).
+// 5.3 TB/s; one row 6.7 us, 64 rows 7.3.  Reading the columns ahead of the reductions did not help (7.0 and 7.5).
+// Dense branches of four vectors a thread spill 36 bytes a lane (fp32, or bf16 rows that are not EVEN) or 100 (such fp32
+// rows): 4096 rows of 20001 bf16 236 us, 176 without a branch.
 template <bool COMBINE, bool BRANCH, bool BF16, bool EVEN, int C, int LANES>
 __global__ __launch_bounds__(1024) void norm_row_kernel(NormArgs a) {
     static_assert(!COMBINE || EVEN, "combine takes rows of a multiple of 8");
